@@ -1,0 +1,404 @@
+"""GPU parity of cache_write, cache_read and decode_cache against the fp64
+definitions.
+
+Codes and scales have to be equal to the definition's.  Decoding, from the
+arithmetic: P is rounded to bf16 (2^-8 of each weight; bf16 cache or prefix) or
+fp16 (2^-11), so O moves by at most that times sum_j p_j |v_j|; a score is a
+sum of D products in fp32, off by at most (D + 16) 2^-23 of its largest sum of
+magnitudes, which moves every weight by that (twice: numerator and sum); the
+exponentials and the fp32 sums add 2^-18; the result is rounded to bf16 (2^-8).
+"""
+import numpy as np
+import pytest
+import torch
+
+from oracle import serving_oracle as so
+from tiled_attention_16_b200 import attention as A
+from tiled_attention_16_b200 import cache, rope
+
+pytestmark = pytest.mark.gpu
+
+BF = torch.finfo(torch.bfloat16).eps / 2
+FMT = {"bf16": torch.bfloat16, "e4m3": torch.float8_e4m3fn, "int8": torch.int8}
+
+
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    return torch.device("cuda:0")
+
+
+def np64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def values(codes, scale):
+    return np64(codes) if scale is None else np64(codes) * np64(scale)[..., None]
+
+
+def new_cache(B, H, cap, D, fmt, dev, fill=True):
+    k, v, ks, vs = cache.make_cache(B, H, cap, D, FMT[fmt], dev)
+    if fill:   # bytes that are NaN as e4m3 and as bf16, NaN scales: nothing may read them
+        for t in (k, v):
+            t.view(torch.uint8).fill_(0xFF)
+        for t in (ks, vs):
+            if t is not None:
+                t.fill_(float("nan"))
+    return k, v, ks, vs
+
+
+def rows(B, H, N, D, seed, token_major=False, sigma=1.0):
+    g = torch.Generator().manual_seed(seed)
+    shape = (B, N, H, D) if token_major else (B, H, N, D)
+    x = (sigma * torch.randn(shape, generator=g)).to(torch.bfloat16).to(_gpu())
+    return x.transpose(1, 2) if token_major else x
+
+
+def ints(*x):
+    return torch.tensor(x, dtype=torch.int32, device=_gpu())
+
+
+# ---------------------------------------------------------------- write, read
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,H,N,cap,D", [(1, 1, 1, 4, 128), (3, 2, 5, 64, 64), (2, 3, 67, 132, 128), (4, 8, 33, 40, 64)])
+def test_write_then_read(fmt, B, H, N, cap, D):
+    dev = _gpu()
+    kc, vc, ks, vs = new_cache(B, H, cap, D, fmt, dev)
+    before = [t.clone() for t in (kc, vc)]
+    k, v = rows(B, H, N, D, 1, sigma=3.0), rows(B, H, N, D, 2, token_major=True, sigma=0.01)
+    start = ints(*[(7 * b) % max(1, cap - N + 1) for b in range(B)])
+    cache.cache_write(k, v, kc, vc, start, k_scale=ks, v_scale=vs)
+    for x, c, s, old in ((k, kc, ks, before[0]), (v, vc, vs, before[1])):
+        codes, scale = (np64(x), None) if fmt == "bf16" else so.quantise_rows(np64(x), fmt)
+        for b in range(B):
+            at = int(start[b])
+            assert (np64(c[b, :, at:at + N]) == codes[b]).all()
+            if s is not None:
+                assert (np64(s[b, :, at:at + N]) == scale[b]).all()
+                assert torch.isnan(s[b, :, :at]).all() and torch.isnan(s[b, :, at + N:]).all()
+            keep = torch.ones(cap, dtype=torch.bool)
+            keep[at:at + N] = False
+            assert torch.equal(c[b].view(torch.uint8)[:, keep], old[b].view(torch.uint8)[:, keep])
+    lens = start + N
+    n = int(lens.max())
+    rk, rv = cache.cache_read(kc[:, :, :], vc, n, lens=lens, k_scale=ks, v_scale=vs)
+    for x, r, f in ((k, rk, ks), (v, rv, vs)):
+        codes, scale = (np64(x), np.ones(x.shape[:3])) if fmt == "bf16" else so.quantise_rows(np64(x), fmt)
+        for b in range(B):
+            at = int(start[b])
+            want = codes[b] * scale[b][..., None]
+            got = np64(r[b, :, at:at + N])
+            # e4m3 values times a power of two are bf16 numbers; int8 ones are rounded (in fp32, then bf16)
+            tol = BF * (1 + 2.0 ** -14) * np.abs(want) if fmt == "int8" else 0.0
+            assert (np.abs(got - want) <= tol).all()
+            assert (r[b, :, at + N:] == 0).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_rounding_over_the_whole_range(fmt):
+    """Rows of every magnitude a bf16 has, ties between codes, largest values at
+    and around the steps of the scale."""
+    dev = _gpu()
+    D, N = 128, 600
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn(1, 1, N, D, generator=g) * torch.exp2(torch.linspace(-132, 120, N))[None, None, :, None]
+    x[0, 0, 0] = 0
+    x[0, 0, 1] = torch.arange(D).float() * 2.0 ** -133                    # subnormal
+    x[0, 0, 2, 0], x[0, 0, 2, 1:] = 3.38e38, 1.0
+    for i, top in enumerate((448.0, 450.0, 446.0, 447.0, 224.0, 1.75, 1.7578125, 127.0, 254.0, 63.5)):
+        x[0, 0, 10 + i] = torch.linspace(-1, 1, D) * top
+        x[0, 0, 10 + i, 0] = top
+    x[0, 0, 30] = (torch.arange(D) - 64).float() + 0.5                    # ties of int8 under a scale of 1 (amax 127)
+    x[0, 0, 30, 0] = 127.0
+    x[0, 0, 31] = torch.arange(D).float() * 2.0 ** -4 + 16                # ties of e4m3
+    x = x.to(torch.bfloat16).to(dev)
+    kc, vc, ks, vs = new_cache(1, 1, N, D, fmt, dev)
+    cache.cache_write(x, x, kc, vc, ints(0), k_scale=ks, v_scale=vs)
+    codes, scale = so.quantise_rows(np64(x), fmt)
+    assert (np64(ks) == scale).all()
+    assert (np64(kc) == codes).all()
+    assert torch.equal(kc.view(torch.uint8), vc.view(torch.uint8)) and torch.equal(ks, vs)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_rows_with_infinities_and_nans_read_back_as_nan(fmt):
+    dev = _gpu()
+    x = rows(1, 2, 6, 64, 9).clone()
+    x[0, 0, 1, 3] = float("inf")
+    x[0, 1, 2, 63] = float("nan")
+    x[0, 1, 4, 0] = -float("inf")
+    kc, vc, ks, vs = new_cache(1, 2, 8, 64, fmt, dev)
+    cache.cache_write(x, x, kc, vc, ints(1), k_scale=ks, v_scale=vs)
+    k, _ = cache.cache_read(kc, vc, 7, lens=ints(7), k_scale=ks, v_scale=vs)
+    bad = torch.zeros(2, 6, dtype=torch.bool, device=dev)
+    bad[0, 1] = bad[1, 2] = bad[1, 4] = True
+    assert torch.isnan(k[0, :, 1:][bad]).all() and torch.isfinite(k[0, :, 1:][~bad]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_rows_without_a_slot_are_dropped(fmt):
+    """Negative starts, starts behind the end, counts below N, 0 and above N."""
+    dev = _gpu()
+    B, H, N, cap, D = 6, 2, 5, 12, 64
+    start, count = ints(-2, 10, 2 ** 31 - 2, -(2 ** 31), 3, 0), ints(5, 9, 5, 5, 2, 0)
+    kc, vc, ks, vs = new_cache(B, H, cap, D, fmt, dev)
+    k, v = rows(B, H, N, D, 3), rows(B, H, N, D, 4)
+    cache.cache_write(k, v, kc, vc, start, count, ks, vs)
+    written = torch.zeros(B, cap, dtype=torch.bool)
+    for b in range(B):
+        for n in range(min(N, int(count[b]))):
+            if 0 <= int(start[b]) + n < cap:
+                written[b, int(start[b]) + n] = True
+    assert written.sum() == 3 + 2 + 2
+    clean = (kc.view(torch.uint8) != 0xFF).any(-1)[:, 0].cpu()
+    assert torch.equal(clean, written)
+    ref = np64(k[0, :, 2:]) if fmt == "bf16" else so.quantise_rows(np64(k[0, :, 2:]), fmt)[0]
+    assert (np64(kc[0, :, :3]) == ref).all()
+
+
+def test_captured_write_follows_the_device_lengths():
+    dev = _gpu()
+    kc, vc, ks, vs = new_cache(2, 2, 16, 128, "e4m3", dev)
+    k, v = rows(2, 2, 1, 128, 1), rows(2, 2, 1, 128, 2)
+    start = ints(0, 3)
+    q = rows(2, 4, 1, 128, 3)
+    cache.cache_write(k, v, kc, vc, start, k_scale=ks, v_scale=vs)
+    vc[1, :, :3], kc[1, :, :3] = 0, 0
+    ks[1, :, :3], vs[1, :, :3] = 1, 1
+    ws = torch.empty(cache.decode_cache_workspace_bytes(2, 4, 2, 1, 16, 128, torch.float8_e4m3fn), device=dev, dtype=torch.uint8)
+    cache.decode_cache(q, kc, vc, start + 1, ks, vs, workspace=ws)
+    torch.cuda.synchronize()
+    lens = start + 1
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        cache.cache_write(k, v, kc, vc, start, k_scale=ks, v_scale=vs)
+        o, lse = cache.decode_cache(q, kc, vc, lens, ks, vs, workspace=ws)
+        start += 1
+        lens += 1
+    for step in range(5):
+        k.copy_(rows(2, 2, 1, 128, 10 + step))
+        v.copy_(rows(2, 2, 1, 128, 20 + step))
+        n = lens.clone()
+        g.replay()
+        torch.cuda.synchronize()
+        want = cache.decode_cache(q, kc, vc, n, ks, vs)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        check_decode(q, kc, vc, ks, vs, n, (o, lse))
+    assert start.tolist() == [5, 8]
+
+
+# ---------------------------------------------------------------- decoding
+
+def check_decode(q, kc, vc, ks, vs, lens, got, causal=True, scale=None, pk=None, pv=None):
+    D = q.shape[-1]
+    scale = D ** -0.5 if scale is None else scale
+    k, v = values(kc, ks), values(vc, vs)
+    for b in range(q.shape[0]):   # what lies behind a length is anything
+        n = min(max(int(lens[b]), 0), k.shape[2])
+        k[b, :, n:], v[b, :, n:] = 0, 0
+    o, lse, wt, size = so.decode_cache(np64(q), k, v, lens.tolist(), scale, causal,
+                                       None if pk is None else np64(pk), None if pv is None else np64(pv))
+    u = BF if ks is None or pk is not None else 2.0 ** -11
+    ds = (D + 16) * 2.0 ** -23 * size
+    go, gl = np64(got[0]), np64(got[1])
+    assert (np.isneginf(gl) == np.isneginf(lse)).all() and (go[np.isneginf(lse)] == 0).all()
+    some = ~np.isneginf(lse)
+    tol = (u * 1.01 + 2 * ds + 2.0 ** -18)[..., None] * wt + BF * 1.01 * np.abs(o)
+    err = np.abs(go - o)
+    assert (err[some] <= tol[some]).all(), f"O off by {(err[some] / tol[some]).max()} of its tolerance"
+    tl = ds + 2.0 ** -18 + 2.0 ** -22 * np.abs(np.where(some, lse, 0))
+    assert (np.abs(gl - np.where(some, lse, 0))[some] <= tl[some]).all()
+
+
+def filled(B, H, cap, D, fmt, lens, dev, seed=1, sk=1.0, sv=1.0):
+    """A cache whose slots below each length were written; the rest is NaN."""
+    kc, vc, ks, vs = new_cache(B, H, cap, D, fmt, dev)
+    n = max(1, min(cap, max(lens)))
+    k, v = rows(B, H, n, D, seed, sigma=sk), rows(B, H, n, D, seed + 1, sigma=sv)
+    cache.cache_write(k, v, kc, vc, ints(*[0] * B), ints(*[max(0, x) for x in lens]), ks, vs)
+    return kc, vc, ks, vs
+
+
+DECODE = [
+    # B, Hq, Hkv, Nq, cap, D, lens, causal
+    (1, 1, 1, 1, 4, 128, [1], True),
+    (1, 2, 1, 1, 64, 64, [64], True),
+    (2, 8, 2, 1, 300, 128, [300, 65], True),
+    (3, 4, 4, 1, 200, 64, [0, 1, 200], True),              # an empty sequence
+    (2, 8, 1, 3, 132, 128, [131, 2], True),                # 24 rows: two row blocks; a row before the first key
+    (2, 12, 4, 5, 260, 64, [3, 259], False),
+    (5, 8, 8, 2, 1000, 128, [17, 1000, 63, 64, 641], True),
+    (1, 40, 8, 1, 2500, 128, [2497], True),
+    (40, 4, 2, 1, 96, 64, [(7 * b) % 97 for b in range(40)], True),
+    (1, 16, 1, 4, 20000, 128, [19999], True),              # 64 rows of one head, many shares of a unit
+    (700, 2, 2, 1, 68, 64, [(5 * b) % 69 for b in range(700)], True),   # more units than CTAs
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,cap,D,lens,causal", DECODE)
+def test_decode_ragged(fmt, B, Hq, Hkv, Nq, cap, D, lens, causal):
+    dev = _gpu()
+    kc, vc, ks, vs = filled(B, Hkv, cap, D, fmt, lens, dev)
+    q = rows(B, Hq, Nq, D, 77)
+    got = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs, causal=causal)
+    assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
+    check_decode(q, kc, vc, ks, vs, ints(*lens), got, causal)
+
+
+PREFIX = [
+    # B, Hq, Hkv, Nq, cap, D, Np, lens
+    (1, 1, 1, 1, 4, 128, 1, [1]),
+    (2, 8, 2, 1, 64, 128, 127, [0, 64]),
+    (3, 4, 2, 2, 100, 64, 128, [100, 5, 1]),
+    (16, 8, 1, 1, 64, 128, 1000, list(range(16))),           # 128 rows: one tile, alternating blocks
+    (17, 8, 1, 1, 64, 128, 385, [64 - b for b in range(17)]),   # 136 rows: two tiles share the keys
+    (33, 8, 2, 2, 32, 64, 700, [b % 33 for b in range(33)]),    # 264 rows: three tiles, the last nearly empty
+    (4, 32, 8, 1, 132, 128, 4100, [1, 130, 50, 90]),
+    (2, 2, 1, 1, 64, 64, 40000, [64, 0]),
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,cap,D,Np,lens", PREFIX)
+def test_decode_behind_a_prefix(fmt, B, Hq, Hkv, Nq, cap, D, Np, lens):
+    dev = _gpu()
+    kc, vc, ks, vs = filled(B, Hkv, cap, D, fmt, lens, dev, seed=31)
+    q = rows(B, Hq, Nq, D, 78)
+    pk, pv = rows(1, Hkv, Np, D, 5)[0].contiguous(), rows(1, Hkv, Np, D, 6)[0].contiguous()
+    got = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs, pk, pv)
+    assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
+    check_decode(q, kc, vc, ks, vs, ints(*lens), got, pk=pk, pv=pv)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("sk,sv,sq", [(1e-3, 1e4, 30.0), (1e4, 1e-6, 1e-4), (1.0, 1e-20, 1.0), (8.0, 1.0, 4.0)])
+def test_decode_scales_of_any_size(fmt, sk, sv, sq):
+    """Scales far from 1, large and tiny logits, V rows of sizes 2^40 apart."""
+    dev = _gpu()
+    lens = [500, 129]
+    kc, vc, ks, vs = filled(2, 2, 512, 128, fmt, lens, dev, sk=sk, sv=sv)
+    vs[0, 0, ::3] *= 2.0 ** 40
+    q = (rows(2, 4, 1, 128, 3).float() * sq).to(torch.bfloat16)
+    got = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs)
+    check_decode(q, kc, vc, ks, vs, ints(*lens), got)
+
+
+def test_zero_queries_and_a_scale_argument():
+    dev = _gpu()
+    for fmt in FMT:
+        kc, vc, ks, vs = filled(2, 1, 128, 64, fmt, [100, 128], dev)
+        q = rows(2, 2, 1, 64, 3).clone()
+        q[0] = 0
+        got = cache.decode_cache(q, kc, vc, ints(100, 128), ks, vs, scale=0.37)
+        check_decode(q, kc, vc, ks, vs, ints(100, 128), got, scale=0.37)
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_poisoned_rows_reach_the_queries_that_see_them_only(fmt):
+    dev = _gpu()
+    lens = [70, 70, 70]
+    kc, vc, ks, vs = filled(3, 1, 128, 64, fmt, lens, dev)
+    ks[0, 0, 69] = float("nan")       # seen by the last query only
+    vs[1, 0, 69] = float("nan")
+    q = rows(3, 2, 2, 64, 3)
+    o, lse = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs)
+    assert torch.isnan(o[:2, :, 1]).all() and torch.isnan(lse[0, :, 1]).all()
+    assert torch.isfinite(o[:2, :, 0]).all() and torch.isfinite(o[2]).all() and torch.isfinite(lse[:, :, 0]).all()
+    ks[2, 0] = float("nan")           # nothing but poison
+    o, lse = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs)
+    assert torch.isnan(o[2]).all() and torch.isnan(lse[2]).all()
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+def test_lengths_out_of_range_are_clamped(fmt):
+    dev = _gpu()
+    B = 4
+    kc, vc, ks, vs = filled(B, 2, 64, 64, fmt, [64] * B, dev)
+    q = rows(B, 2, 1, 64, 3)
+    got = cache.decode_cache(q, kc, vc, ints(-5, 1000, 2 ** 31 - 1, -(2 ** 31)), ks, vs)
+    want = cache.decode_cache(q, kc, vc, ints(0, 64, 64, 0), ks, vs)
+    assert A.device_status(dev) == A.FA_OK
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert (got[0][0] == 0).all() and torch.isneginf(got[1][0]).all()
+
+
+def test_repeated_calls_and_streams_are_bitwise_equal():
+    dev = _gpu()
+    lens = ints(777, 20, 1500)
+    kc, vc, ks, vs = filled(3, 2, 1504, 128, "e4m3", lens.tolist(), dev)
+    q = rows(3, 8, 1, 128, 3)
+    pk, pv = rows(1, 2, 900, 128, 5)[0].contiguous(), rows(1, 2, 900, 128, 6)[0].contiguous()
+    want = cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(4)]
+    res = []
+    for s in streams:
+        with torch.cuda.stream(s):
+            for _ in range(5):
+                res.append(cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv))
+    torch.cuda.synchronize()
+    assert all(torch.equal(r[0], want[0]) and torch.equal(r[1], want[1]) for r in res)
+
+
+def test_bf16_cache_agrees_with_decode():
+    """Full lengths: the same attention as decode over the same history."""
+    dev = _gpu()
+    k, v, q = rows(2, 2, 640, 128, 1), rows(2, 2, 640, 128, 2), rows(2, 8, 3, 128, 3)
+    a = A.decode(q, k, v, causal=True)
+    b = cache.decode_cache(q, k, v, ints(640, 640))
+    assert (a[0].float() - b[0].float()).abs().max() <= 2e-2 and (a[1] - b[1]).abs().max() <= 1e-3
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+def test_prefix_equals_a_copy_in_every_cache(fmt):
+    """A shared prefix gives what a copy of it in front of each sequence's own
+    rows gives (bf16 caches: the same numbers go in)."""
+    dev = _gpu()
+    B, Hq, Hkv, D, Np, n = 3, 6, 2, 64, 200, 50
+    pk, pv = rows(1, Hkv, Np, D, 5), rows(1, Hkv, Np, D, 6)
+    k, v, q = rows(B, Hkv, n, D, 7), rows(B, Hkv, n, D, 8), rows(B, Hq, 2, D, 9)
+    own = new_cache(B, Hkv, 64, D, fmt, dev)
+    cache.cache_write(k, v, own[0], own[1], ints(0, 0, 0), k_scale=own[2], v_scale=own[3])
+    a = cache.decode_cache(q, own[0], own[1], ints(n, n, n), own[2], own[3], pk[0].contiguous(), pv[0].contiguous())
+    back = cache.cache_read(own[0], own[1], n, k_scale=own[2], v_scale=own[3])
+    both = [torch.cat([p.expand(B, -1, -1, -1), x], 2).contiguous() for p, x in zip((pk, pv), back)]
+    b = cache.decode_cache(q, both[0], both[1], ints(*[Np + n] * 3))
+    assert (a[0].float() - b[0].float()).abs().max() <= 2e-2 and (a[1] - b[1]).abs().max() <= 2e-3
+
+
+def test_tokens_through_norm_cache_and_decoding():
+    """Serving as it is used: the prompt goes through qk_norm_rope and fwd and
+    into an 8-bit cache; each new token through qk_norm_rope, cache_write and
+    decode_cache behind a shared prefix; the history reads back."""
+    dev = _gpu()
+    B, Hq, Hkv, D, Np, N = 2, 4, 2, 128, 150, 70
+    g = torch.Generator().manual_seed(4)
+    w = [(1 + 0.1 * torch.randn(D, generator=g)).to(dev) for _ in range(2)]
+    inv = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().to(dev)
+
+    def project(b, n):
+        x = torch.randn(b, n, Hq + 2 * Hkv, D, generator=g).to(torch.bfloat16).to(dev).transpose(1, 2)
+        return x[:, :Hq], x[:, Hq:Hq + Hkv], x[:, Hq + Hkv:]
+
+    def place(b, n, at):
+        return (torch.arange(n, dtype=torch.int32)[None] + at).expand(b, n).contiguous().to(dev)
+
+    _, pk, pv = project(1, Np)
+    pk = rope.qk_norm_rope(pk, pk, w[1], w[1], inv, positions=place(1, Np, 0))[0][0]
+    pv = pv[0].contiguous()
+    kc, vc, ks, vs = new_cache(B, Hkv, 128, D, "e4m3", dev)
+    lens = ints(0, 0)
+    for at, n in ((0, N), (N, 1), (N + 1, 1), (N + 2, 3)):
+        q, k, v = project(B, n)
+        q, k = rope.qk_norm_rope(q, k, w[0], w[1], inv, positions=place(B, n, Np + at))
+        cache.cache_write(k, v, kc, vc, lens, k_scale=ks, v_scale=vs)
+        lens = lens + n
+        got = cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv)
+        assert A.device_status(dev) == A.FA_OK
+        check_decode(q, kc, vc, ks, vs, lens, got, pk=pk, pv=pv)
+    hk, hv = cache.cache_read(kc, vc, int(lens[0]), lens=lens, k_scale=ks, v_scale=vs)
+    assert (np64(hk) == values(kc, ks)[:, :, :int(lens[0])]).all()
+    o, lse = A.fwd(hk, hk, hv, causal=True)     # the history as the next chunk's forward takes it
+    assert torch.isfinite(o).all() and torch.isfinite(lse).all()

@@ -100,11 +100,16 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
-def declared_symbols() -> list[str]:
-    """Entry points declared in include/fa.h (FA_API functions)."""
-    with open(HEADER_PATH) as f:
+def symbols_in(header: str) -> list[str]:
+    """Entry points (FA_API functions) that a header of the library declares."""
+    with open(header) as f:
         text = f.read()
     return re.findall(r"FA_API\s+[\w\s\*]+?\b(fa_\w+)\s*\(", text)
+
+
+def declared_symbols() -> list[str]:
+    """Entry points declared in include/fa.h (FA_API functions)."""
+    return symbols_in(HEADER_PATH)
 
 
 def status_str(status: int) -> str:

@@ -14,8 +14,10 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfa_sm100.so")
-SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_bwd_split.cu", "fa_bwd_fused.cu", "fa_bwd_pair.cu", "fa_decode.cu", "fa_cp.cu", "fa_selftest.cu"]
+SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_bwd_split.cu", "fa_bwd_fused.cu", "fa_bwd_pair.cu", "fa_decode.cu", "fa_cp.cu", "fa_selftest.cu",
+           "fa_rope.cu", "fa_cache.cu", "fa_cache_decode.cu", "fa_prefix.cu", "fa_cache_api.cu"]
 HEADERS = ["sm100.cuh", "fa_internal.h"]
+PUBLIC = ["fa.h", "fa_rope.h", "fa_cache.h"]
 
 NVCC_FLAGS = [
     "-gencode", "arch=compute_100a,code=sm_100a",
@@ -36,7 +38,7 @@ def _stale() -> bool:
     if not os.path.exists(LIB):
         return True
     t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", "fa.h")]
+    deps = [os.path.join(CSRC, f) for f in SOURCES + HEADERS] + [os.path.join(ROOT, "include", h) for h in PUBLIC]
     return any(os.path.getmtime(d) > t for d in deps)
 
 

@@ -34,27 +34,32 @@ PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
     return fn;
 }
 
+}  // namespace
+
 // 3-D map over a contiguous [BH, N, D] tensor: box = 128 bytes of a row
-// (64 bf16 or 128 e4m3) x 128 rows x 1 head, 128-byte swizzle; rows past N
-// read as zero.
-bool make_map(CUtensorMap* map, const void* base, int BH, int N, int D, int elem_bytes = 2, int box_rows = kTileM) {
+// (64 bf16 or 128 one-byte elements; 64 bytes of a 64-byte row) x box_rows rows
+// x 1 head, swizzled over the box's width; rows past N read as zero.
+bool make_map(CUtensorMap* map, const void* base, int BH, int N, int D, int elem_bytes, int box_rows) {
     auto fn = encode_fn();
     if (!fn) return false;
     const cuuint64_t eb = static_cast<cuuint64_t>(elem_bytes);
     cuuint64_t dims[3] = {static_cast<cuuint64_t>(D), static_cast<cuuint64_t>(N), static_cast<cuuint64_t>(BH)};
     cuuint64_t strides[2] = {static_cast<cuuint64_t>(D) * eb, static_cast<cuuint64_t>(N) * D * eb};
-    cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / elem_bytes), static_cast<cuuint32_t>(box_rows), 1};
+    const bool narrow = D * elem_bytes < 128;
+    cuuint32_t box[3] = {static_cast<cuuint32_t>(narrow ? D : 128 / elem_bytes), static_cast<cuuint32_t>(box_rows), 1};
     cuuint32_t estr[3] = {1, 1, 1};
     const CUtensorMapDataType dt = elem_bytes == 1 ? CU_TENSOR_MAP_DATA_TYPE_UINT8 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
-    CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr,
-                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    CUresult r = fn(map, dt, 3, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                    narrow ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS;
 }
 
 bool aligned16(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 // fp32 vectors read or written one element at a time
 bool aligned4(const void* p) { return p != nullptr && (reinterpret_cast<uintptr_t>(p) & 3u) == 0; }
+
+namespace {
 
 fa_status check_shape(const fa_shape* s) {
     if (!s) return FA_ERR_INVALID_ARG;
@@ -90,6 +95,8 @@ fa_status check_device() {
 unsigned int g_last_sites = 0;
 
 }  // namespace
+
+int device_status_code() { return check_device(); }
 
 int sm_count() {
     static int cache[64] = {};

@@ -1,0 +1,230 @@
+// fa_cache.cu — writing K/V rows into a cache at 16 or 8 bits, and reading
+// them back (include/fa_cache.h has the formats and the rounding rules).
+//
+// Bound by HBM: a write reads 2 bytes an element and writes 1 or 2, a read the
+// other way round.  D / 8 lanes hold a row, 8 values each (16-byte accesses on
+// the bf16 side, 8-byte on the codes); a thread takes kRows rows and issues
+// their loads together.  blockIdx.y is 0 for K and 1 for V.
+#include "fa_internal.h"
+#include "sm100.cuh"
+
+#include <cuda_bf16.h>
+#include <cuda_fp8.h>
+
+namespace fa {
+
+namespace {
+
+constexpr int kCacheThreads = 256;
+constexpr int kRows = 4;
+
+__device__ __forceinline__ float bf16_lo(uint32_t w) { return __uint_as_float(w << 16); }
+__device__ __forceinline__ float bf16_hi(uint32_t w) { return __uint_as_float(w & 0xffff0000u); }
+
+// Largest magnitude of the row as bf16 bits (sign cleared); infinities and
+// NaNs are the values from 0x7f80 on, so they win the integer maximum.
+template <int kLanes>
+__device__ __forceinline__ uint32_t row_amax_bits(const uint4& w) {
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    uint32_t m = __vmaxu2(__vmaxu2(w.x & kAbs, w.y & kAbs), __vmaxu2(w.z & kAbs, w.w & kAbs));
+#pragma unroll
+    for (int k = kLanes / 2; k; k >>= 1) m = __vmaxu2(m, __shfl_xor_sync(0xffffffffu, m, k));
+    return max(m & 0xffffu, m >> 16);
+}
+
+// 8 values to e4m3 codes.  The scale is 2^e with the smallest e >= -120 such
+// that amax <= 448 * 2^e = 1.75 * 2^(8 + e): from the exponent and the seven
+// mantissa bits of amax.  Multiplying by 2^-e is exact (values that leave the
+// fp32 range downwards are far below half of the smallest code), so a value is
+// rounded once, by the conversion.
+__device__ __forceinline__ uint2 codes_e4m3(const uint4& w, uint32_t amax, float& scale) {
+    int e = static_cast<int>(amax >> 7) - 127 - 8 + ((amax & 0x7fu) > 0x60u ? 1 : 0);
+    e = max(e, -120);
+    scale = __int_as_float((127 + e) << 23);
+    const float inv = __int_as_float((127 - e) << 23);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t c[2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(bf16_lo(v[2 * i]) * inv, bf16_hi(v[2 * i]) * inv),
+                                                     __NV_SATFINITE, __NV_E4M3);
+        const uint32_t hi = __nv_cvt_float2_to_fp8x2(
+            make_float2(bf16_lo(v[2 * i + 1]) * inv, bf16_hi(v[2 * i + 1]) * inv), __NV_SATFINITE, __NV_E4M3);
+        c[i] = lo | (hi << 16);
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+// Nearest integer to x / s, ties to even, exactly: x times the rounded 1 / s
+// gives the integer up to one, and the residual x - q s is exact in fp32 (x has
+// 8 significant bits and |x| >= s / 2 where q != 0, so it is a multiple of s's
+// last bit below 2 s), so comparing it with s / 2 settles the rest.
+__device__ __forceinline__ int code_int8(float x, float s, float inv) {
+    const float q = rintf(x * inv);
+    const float r = fmaf(-q, s, x), h = 0.5f * s;
+    int i = static_cast<int>(q);
+    const int odd = i & 1;
+    if (r > h || (r == h && odd)) ++i;
+    if (r < -h || (r == -h && odd)) --i;
+    return i;
+}
+
+__device__ __forceinline__ uint2 codes_int8(const uint4& w, uint32_t amax, float& scale) {
+    scale = fmaxf(__fdiv_rn(__uint_as_float(amax << 16), 127.f), 7.52316385e-37f);   // 2^-120
+    const float inv = __fdiv_rn(1.f, scale);
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    uint32_t c[2] = {0u, 0u};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t lo = static_cast<uint32_t>(code_int8(bf16_lo(v[i]), scale, inv)) & 0xffu;
+        const uint32_t hi = static_cast<uint32_t>(code_int8(bf16_hi(v[i]), scale, inv)) & 0xffu;
+        c[i >> 1] |= (lo | (hi << 8)) << (16 * (i & 1));
+    }
+    return make_uint2(c[0], c[1]);
+}
+
+template <int D, int kFmt>
+__global__ void __launch_bounds__(kCacheThreads)
+fa_cache_write_kernel(const CacheWriteParams p) {
+    constexpr int kLanes = D / 8;
+    constexpr int kSlots = kCacheThreads / kLanes;
+    const int lane = threadIdx.x & (kLanes - 1);
+    const RopeRows& x = blockIdx.y ? p.v : p.k;
+    uint8_t* cache = static_cast<uint8_t*>(blockIdx.y ? p.v_cache : p.k_cache);
+    float* scales = blockIdx.y ? p.v_scale : p.k_scale;
+    const long long first = static_cast<long long>(blockIdx.x) * (kSlots * kRows) + threadIdx.x / kLanes;
+    uint4 raw[kRows];
+    long long slot[kRows];   // row of the cache, -1: not written
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const long long row = first + i * kSlots;
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);
+        slot[i] = -1;
+        if (row < p.rows) {
+            const unsigned bh = static_cast<unsigned>(row) / static_cast<unsigned>(p.N);
+            const int n = static_cast<int>(static_cast<unsigned>(row) - bh * static_cast<unsigned>(p.N));
+            const int b = static_cast<int>(bh / static_cast<unsigned>(p.H));
+            const int h = static_cast<int>(bh - static_cast<unsigned>(b) * static_cast<unsigned>(p.H));
+            raw[i] = __ldg(reinterpret_cast<const uint4*>(x.data + b * x.stride_b + h * x.stride_h + n * x.stride_n) +
+                           lane);
+            const long long at = static_cast<long long>(__ldg(p.start + b)) + n;
+            const int cnt = p.count ? __ldg(p.count + b) : p.N;
+            if (n < cnt && at >= 0 && at < p.capacity) slot[i] = static_cast<long long>(bh) * p.capacity + at;
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        if constexpr (kFmt == 0) {
+            if (slot[i] >= 0) *(reinterpret_cast<uint4*>(cache + slot[i] * (2 * D)) + lane) = raw[i];
+        } else {
+            const uint32_t amax = row_amax_bits<kLanes>(raw[i]);
+            float scale;
+            uint2 c = kFmt == 1 ? codes_e4m3(raw[i], amax, scale) : codes_int8(raw[i], amax, scale);
+            if (amax >= 0x7f80u) {   // an infinity or a NaN: the whole row reads back as NaN
+                c = make_uint2(0u, 0u);
+                scale = __uint_as_float(0x7fc00000u);
+            }
+            if (slot[i] >= 0) {
+                *(reinterpret_cast<uint2*>(cache + slot[i] * D) + lane) = c;
+                if (lane == 0) scales[slot[i]] = scale;
+            }
+        }
+    }
+}
+
+template <int D, int kFmt>
+__global__ void __launch_bounds__(kCacheThreads)
+fa_cache_read_kernel(const CacheReadParams p) {
+    constexpr int kLanes = D / 8;
+    constexpr int kSlots = kCacheThreads / kLanes;
+    const int lane = threadIdx.x & (kLanes - 1);
+    const uint8_t* cache = static_cast<const uint8_t*>(blockIdx.y ? p.v_cache : p.k_cache);
+    const float* scales = blockIdx.y ? p.v_scale : p.k_scale;
+    __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.y ? p.v_out : p.k_out);
+    const long long first = static_cast<long long>(blockIdx.x) * (kSlots * kRows) + threadIdx.x / kLanes;
+    uint4 raw[kRows];
+    float scale[kRows];
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const long long row = first + i * kSlots;
+        raw[i] = make_uint4(0u, 0u, 0u, 0u);   // rows behind the length: codes 0, scale 0
+        scale[i] = 0.f;
+        if (row < p.rows) {
+            const unsigned bh = static_cast<unsigned>(row) / static_cast<unsigned>(p.N);
+            const int n = static_cast<int>(static_cast<unsigned>(row) - bh * static_cast<unsigned>(p.N));
+            const int len = p.lens ? __ldg(p.lens + bh / static_cast<unsigned>(p.H)) : p.capacity;
+            if (n < len) {
+                const long long slot = static_cast<long long>(bh) * p.capacity + n;
+                if constexpr (kFmt == 0) {
+                    raw[i] = __ldg(reinterpret_cast<const uint4*>(cache + slot * (2 * D)) + lane);
+                } else {
+                    const uint2 c = __ldg(reinterpret_cast<const uint2*>(cache + slot * D) + lane);
+                    raw[i].x = c.x;
+                    raw[i].y = c.y;
+                    scale[i] = __ldg(scales + slot);
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kRows; ++i) {
+        const long long row = first + i * kSlots;
+        if (row >= p.rows) break;
+        uint4 o = raw[i];
+        if constexpr (kFmt != 0) {
+            const uint32_t c[2] = {raw[i].x, raw[i].y};
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const uint32_t two = c[j >> 1] >> (16 * (j & 1));
+                float2 f;
+                if constexpr (kFmt == 1) {
+                    const __half2_raw hr =
+                        __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(two & 0xffffu), __NV_E4M3);
+                    f = __half22float2(__half2(hr));
+                } else {
+                    f = make_float2(static_cast<float>(static_cast<int8_t>(two & 0xffu)),
+                                    static_cast<float>(static_cast<int8_t>((two >> 8) & 0xffu)));
+                }
+                w[j] = pack_bf16x2(f.x * scale[i], f.y * scale[i]);
+            }
+            o = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *(reinterpret_cast<uint4*>(out + row * D) + lane) = o;
+    }
+}
+
+template <class F>
+cudaError_t cache_dispatch(int D, int fmt, F&& go) {
+    auto with_d = [&](auto d) {
+        if (fmt == 0) return go(d, std::integral_constant<int, 0>{});
+        if (fmt == 1) return go(d, std::integral_constant<int, 1>{});
+        return go(d, std::integral_constant<int, 2>{});
+    };
+    return D == 128 ? with_d(std::integral_constant<int, 128>{}) : with_d(std::integral_constant<int, 64>{});
+}
+
+dim3 cache_grid(int D, long long rows) {
+    const int per = kCacheThreads / (D / 8) * kRows;
+    return dim3(static_cast<unsigned>((rows + per - 1) / per), 2);
+}
+
+}  // namespace
+
+cudaError_t launch_cache_write(int D, int fmt, const CacheWriteParams& p, cudaStream_t stream) {
+    return cache_dispatch(D, fmt, [&](auto d, auto f) {
+        fa_cache_write_kernel<decltype(d)::value, decltype(f)::value>
+            <<<cache_grid(D, p.rows), kCacheThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    });
+}
+
+cudaError_t launch_cache_read(int D, int fmt, const CacheReadParams& p, cudaStream_t stream) {
+    return cache_dispatch(D, fmt, [&](auto d, auto f) {
+        fa_cache_read_kernel<decltype(d)::value, decltype(f)::value>
+            <<<cache_grid(D, p.rows), kCacheThreads, 0, stream>>>(p);
+        return cudaGetLastError();
+    });
+}
+
+}  // namespace fa

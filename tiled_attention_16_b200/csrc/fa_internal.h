@@ -4,6 +4,7 @@
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
+#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace fa {
@@ -39,6 +40,16 @@ struct FwdParams {
 
 // Multiprocessor count of the current device (cached per device; -1 on error).
 int sm_count();
+
+// Host helpers of the entry points (fa_api.cu): pointer checks, and whether the
+// current device is an sm_100 (an fa_status; cached per device).
+bool aligned16(const void* p);
+bool aligned4(const void* p);
+int device_status_code();
+// 3-D map over a contiguous [BH, N, D] tensor with a box of 128 bytes of a row
+// (64 bytes where the row is no longer: 64-byte swizzle there, else 128-byte)
+// x box_rows rows x 1 head; rows past N read as zero.
+bool make_map(CUtensorMap* map, const void* base, int BH, int N, int D, int elem_bytes = 2, int box_rows = kTileM);
 
 struct BwdParams {
     int B, Hq, Hkv, N, Npad;
@@ -148,5 +159,87 @@ cudaError_t launch_bwd_dq_convert(const float* dq_acc, void* dq, size_t n_elems,
 cudaError_t launch_lse_merge(int D, long long rows, const void* o_part, const float* lse_part, float* o_acc,
                              float* lse_acc, void* o_out, int first, cudaStream_t stream);
 cudaError_t launch_accumulate(long long n, const void* src, float* acc, void* out, int first, cudaStream_t stream);
+
+// bf16 rows of D contiguous values, indexed [b, h, n] by strides in elements.
+struct RopeRows {
+    __nv_bfloat16* data;
+    long long stride_b, stride_h, stride_n;
+};
+
+// Per-head norm with rotation (fa_rope.cu); q_out / k_out are written by the
+// forward, the d* fields are the backward's.
+struct RopeParams {
+    RopeRows q, k, dq, dk;
+    __nv_bfloat16 *q_out, *k_out;
+    const __nv_bfloat16 *dq_out, *dk_out;
+    const void *q_weight, *k_weight;
+    const float* inv_freq;
+    const int* positions;
+    float* dw_part;    // [CTAs, 2, D]
+    int Hq, Hkv, N, rot, weight_bf16;
+    float eps;
+    long long tokens;  // B * N
+    int token_slots, head_parts, n_items;   // filled by the launch
+};
+int rope_bwd_ctas(int sms);
+cudaError_t launch_qk_norm_rope(int D, int interleaved, RopeParams p, int sms, cudaStream_t stream);
+cudaError_t launch_qk_norm_rope_bwd(int D, int interleaved, RopeParams p, float* dqw, float* dkw, int sms,
+                                    cudaStream_t stream);
+
+// Cache writes and reads (fa_cache.cu); rows = B * H * N.
+struct CacheWriteParams {
+    RopeRows k, v;
+    const int *start, *count;
+    void *k_cache, *v_cache;
+    float *k_scale, *v_scale;
+    int H, N, capacity;
+    long long rows;
+};
+struct CacheReadParams {
+    const void *k_cache, *v_cache;
+    const float *k_scale, *v_scale;
+    const int* lens;
+    void *k_out, *v_out;
+    int H, N, capacity;
+    long long rows;
+};
+cudaError_t launch_cache_write(int D, int fmt, const CacheWriteParams& p, cudaStream_t stream);
+cudaError_t launch_cache_read(int D, int fmt, const CacheReadParams& p, cudaStream_t stream);
+
+// Decoding over a cache (fa_cache_decode.cu).
+struct CacheDecodeParams {
+    const void* q;           // bf16 [B,Hq,Nq,D]
+    void* o;                 // bf16 [B,Hq,Nq,D]
+    float* lse;              // fp32 [B,Hq,Nq]
+    const int* lens;
+    const float *k_scale, *v_scale;
+    float *o_part, *lse_part;  // parts of units shared by CTAs: slots 2 c, 2 c + 1 of rows_cta rows each
+    float *o_unit, *lse_unit;  // [B*Hq*Nq, D], [B*Hq*Nq]: undivided units' results for the merge with the
+                               // prefix (null without one: they go to o and lse)
+    int2* meta;              // [B * HR]: first slot (-1: undivided), last CTA of the unit
+    int B, Hkv, G, Nq, capacity, causal;
+    int rows_cta, RB, HR;    // query rows a CTA holds (8 or 16), row blocks of a K/V head, Hkv * RB
+    int n_cta;
+    float scale_log2;
+};
+// CTAs of the cache part that fit on an SM at once (shared memory and registers).
+int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta);
+cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
+                                const CacheDecodeParams& p, cudaStream_t stream);
+
+// Shared prefix (fa_prefix.cu).  A unit is rows_unit of the B * G * Nq rows of
+// a K/V head; the part of unit u that CTA c computes lies in slot c + u of
+// 256 rows: rows_unit rows of each of its `subs` partial results.
+struct PrefixParams {
+    const void* q;
+    float *o_part, *lse_part;
+    int B, Hkv, G, Nq, Np;
+    int rows_unit, subs, n_rowtiles, n_tiles;
+    int n_cta;               // 0: no prefix
+    float scale_log2;
+};
+cudaError_t launch_prefix(int D, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& p,
+                          cudaStream_t stream);
+cudaError_t launch_cache_combine(int D, const CacheDecodeParams& p, const PrefixParams& f, cudaStream_t stream);
 
 }  // namespace fa
