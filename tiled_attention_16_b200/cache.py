@@ -12,13 +12,15 @@ is missing or the device is not a B200 the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import math
 import os
 
 import torch
 
-from .attention import FA_OK, FAError, _check, _same_device, _stream_ptr, lib, symbols_in
-from .rope import FaRows, _ptr, check_rows
+from ._args import on_device, raw_stream, want
+from .attention import FA_OK, FAError, lib, symbols_in
+from .rope import FaRows, check_rows
 
 HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "fa_cache.h")
 
@@ -74,25 +76,26 @@ def make_cache(B: int, Hkv: int, capacity: int, D: int, dtype=torch.bfloat16, de
     return k, v, ks, vs
 
 
-def _check_cache(k_cache, v_cache, k_scale, v_scale) -> int:
-    """The caches' format, after checks of the four tensors."""
+def _check_cache(k_cache, v_cache, k_scale, v_scale):
+    """(format, address of k_scale, of v_scale) after checks of the four tensors."""
     if not isinstance(k_cache, torch.Tensor) or k_cache.dim() != 4:
         raise ValueError("k_cache must be [B, Hkv, capacity, D]")
     dt = k_cache.dtype
-    if dt not in FORMATS:
+    fmt = FORMATS.get(dt)
+    if fmt is None:
         raise TypeError(f"k_cache must be one of {list(FORMATS)}, got {dt}")
     shape = k_cache.shape
-    _check(k_cache, "k_cache", shape, dt)
-    _check(v_cache, "v_cache", shape, dt)
-    if dt == torch.bfloat16:
+    want(k_cache, "k_cache", shape, dt, k_cache)
+    want(v_cache, "v_cache", shape, dt, k_cache)
+    if fmt == 0:
         if k_scale is not None or v_scale is not None:
             raise ValueError("a bf16 cache has no scales")
-    else:
-        if k_scale is None or v_scale is None:
-            raise ValueError(f"a {dt} cache needs k_scale and v_scale")
-        _check(k_scale, "k_scale", shape[:3], torch.float32)
-        _check(v_scale, "v_scale", shape[:3], torch.float32)
-    return FORMATS[dt]
+        return 0, None, None
+    if k_scale is None or v_scale is None:
+        raise ValueError(f"a {dt} cache needs k_scale and v_scale")
+    want(k_scale, "k_scale", shape[:3], torch.float32, k_cache)
+    want(v_scale, "v_scale", shape[:3], torch.float32, k_cache)
+    return fmt, k_scale.data_ptr(), v_scale.data_ptr()
 
 
 def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, start: torch.Tensor,
@@ -102,23 +105,27 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     sequence b, for n < count[b] (int32 [B] tensors; default count: N),
     quantised row by row where the cache holds 8 bits.  Rows whose slot is
     outside the cache are dropped; all other slots stay as they are."""
-    fmt = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    fmt, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
     B, Hkv, cap, D = k_cache.shape
     if k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, D]")
     N = k.shape[2]
-    kr, vr = check_rows(k, "k", (B, Hkv, N, D)), check_rows(v, "v", (B, Hkv, N, D))
-    _check(start, "start", (B,), torch.int32)
+    shape = (B, Hkv, N, D)
+    kr, vr = check_rows(k, "k", shape, k_cache), check_rows(v, "v", shape, k_cache)
+    want(start, "start", (B,), torch.int32, k_cache)
     if count is not None:
-        _check(count, "count", (B,), torch.int32)
+        want(count, "count", (B,), torch.int32, k_cache)
     if N == 0:
         return
-    dev = _same_device(k, v, k_cache, v_cache, start, count, k_scale, v_scale)
+    index = k_cache.get_device()
+    guard = on_device(index)
+    if guard is not None:
+        with guard:
+            return cache_write(k, v, k_cache, v_cache, start, count, k_scale, v_scale)
     shp = FaCacheShape(B, Hkv, cap, D, fmt)
-    with torch.cuda.device(dev):
-        st = _cache_lib().fa_cache_write(ctypes.byref(shp), N, ctypes.byref(kr), ctypes.byref(vr), start.data_ptr(),
-                                         _ptr(count), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
-                                         _ptr(v_scale), _stream_ptr(dev))
+    st = _cache_lib().fa_cache_write(ctypes.byref(shp), N, ctypes.byref(kr), ctypes.byref(vr), start.data_ptr(),
+                                     None if count is None else count.data_ptr(), k_cache.data_ptr(),
+                                     v_cache.data_ptr(), ks, vs, raw_stream(index))
     if st != FA_OK:
         raise FAError(st, "fa_cache_write")
 
@@ -128,25 +135,40 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, n: int | None = Non
                out_k: torch.Tensor | None = None, out_v: torch.Tensor | None = None):
     """The first n slots (default: all) of every sequence as bf16
     (k [B,Hkv,n,D], v); rows at or behind lens[b] (int32 [B]) are 0."""
-    fmt = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    fmt, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
     B, Hkv, cap, D = k_cache.shape
     n = cap if n is None else int(n)
     if lens is not None:
-        _check(lens, "lens", (B,), torch.int32)
+        want(lens, "lens", (B,), torch.int32, k_cache)
     shape = (B, Hkv, n, D)
-    out_k = torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) if out_k is None else out_k
-    out_v = torch.empty(shape, device=k_cache.device, dtype=torch.bfloat16) if out_v is None else out_v
-    _check(out_k, "out_k", shape)
-    _check(out_v, "out_v", shape)
-    dev = _same_device(k_cache, v_cache, lens, k_scale, v_scale, out_k, out_v)
+    index = k_cache.get_device()
+    guard = on_device(index)
+    if guard is not None:
+        with guard:
+            return cache_read(k_cache, v_cache, n, lens, k_scale, v_scale, out_k, out_v)
+    if out_k is None:
+        out_k = k_cache.new_empty(shape, dtype=torch.bfloat16)
+    else:
+        want(out_k, "out_k", shape, torch.bfloat16, k_cache)
+    if out_v is None:
+        out_v = k_cache.new_empty(shape, dtype=torch.bfloat16)
+    else:
+        want(out_v, "out_v", shape, torch.bfloat16, k_cache)
     shp = FaCacheShape(B, Hkv, cap, D, fmt)
-    with torch.cuda.device(dev):
-        st = _cache_lib().fa_cache_read(ctypes.byref(shp), n, _ptr(lens), k_cache.data_ptr(), v_cache.data_ptr(),
-                                        _ptr(k_scale), _ptr(v_scale), out_k.data_ptr(), out_v.data_ptr(),
-                                        _stream_ptr(dev))
+    st = _cache_lib().fa_cache_read(ctypes.byref(shp), n, None if lens is None else lens.data_ptr(),
+                                    k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, out_k.data_ptr(),
+                                    out_v.data_ptr(), raw_stream(index))
     if st != FA_OK:
         raise FAError(st, "fa_cache_read")
     return out_k, out_v
+
+
+@functools.lru_cache(maxsize=1024)
+def _decode_shape(index, *fields):
+    """The C shape and its workspace (at least 256 bytes, so that what is
+    wrong with a refused shape is the library's to report)."""
+    shp = FaCacheDecodeShape(*fields)
+    return shp, max(int(_cache_lib().fa_decode_cache_workspace_bytes(ctypes.byref(shp))), 256)
 
 
 def decode_cache_workspace_bytes(B, Hq, Hkv, Nq, capacity, D, dtype=torch.bfloat16, n_prefix=0) -> int:
@@ -169,38 +191,48 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     query that sees no key gets 0 and -inf."""
     if q.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, D]")
-    fmt = _check_cache(k_cache, v_cache, k_scale, v_scale)
+    fmt, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
     _, Hkv, cap, D = k_cache.shape
     B, Hq, Nq, _ = q.shape
-    _check(q, "q", (B, Hq, Nq, D))
+    want(q, "q", (B, Hq, Nq, D), torch.bfloat16, k_cache)
     if k_cache.shape[0] != B:
         raise ValueError(f"k_cache has {k_cache.shape[0]} sequences, q has {B}")
-    _check(lens, "lens", (B,), torch.int32)
-    n_prefix = 0
+    want(lens, "lens", (B,), torch.int32, k_cache)
+    n_prefix, pk, pv = 0, None, None
     if prefix_k is not None or prefix_v is not None:
         if prefix_k is None or prefix_v is None:
             raise ValueError("prefix_k and prefix_v come together")
         if prefix_k.dim() != 3:
             raise ValueError("prefix_k must be [Hkv, Np, D]")
         n_prefix = prefix_k.shape[1]
-        _check(prefix_k, "prefix_k", (Hkv, n_prefix, D))
-        _check(prefix_v, "prefix_v", (Hkv, n_prefix, D))
-    scale = 1.0 / math.sqrt(D) if scale is None else float(scale)
-    out = torch.empty_like(q) if out is None else out
-    lse = torch.empty((B, Hq, Nq), device=q.device, dtype=torch.float32) if lse is None else lse
-    _check(out, "out", (B, Hq, Nq, D))
-    _check(lse, "lse", (B, Hq, Nq), torch.float32)
-    dev = _same_device(q, k_cache, v_cache, lens, k_scale, v_scale, prefix_k, prefix_v, out, lse, workspace)
-    shp = FaCacheDecodeShape(B, Hq, Hkv, Nq, cap, n_prefix, D, fmt, scale, 1 if causal else 0)
-    with torch.cuda.device(dev):
-        L = _cache_lib()
-        if workspace is None:
-            nbytes = int(L.fa_decode_cache_workspace_bytes(ctypes.byref(shp)))
-            workspace = torch.empty(max(nbytes, 256), device=dev, dtype=torch.uint8)
-        st = L.fa_decode_cache(ctypes.byref(shp), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(k_scale),
-                               _ptr(v_scale), lens.data_ptr(), _ptr(prefix_k), _ptr(prefix_v), out.data_ptr(),
-                               lse.data_ptr(), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                               _stream_ptr(dev))
+        want(prefix_k, "prefix_k", (Hkv, n_prefix, D), torch.bfloat16, k_cache)
+        want(prefix_v, "prefix_v", (Hkv, n_prefix, D), torch.bfloat16, k_cache)
+        pk, pv = prefix_k.data_ptr(), prefix_v.data_ptr()
+    index = k_cache.get_device()
+    guard = on_device(index)
+    if guard is not None:
+        with guard:
+            return decode_cache(q, k_cache, v_cache, lens, k_scale, v_scale, prefix_k, prefix_v, causal, scale, out,
+                                lse, workspace)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        want(out, "out", (B, Hq, Nq, D), torch.bfloat16, k_cache)
+    if lse is None:
+        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+    else:
+        want(lse, "lse", (B, Hq, Nq), torch.float32, k_cache)
+    shp, nbytes = _decode_shape(index, B, Hq, Hkv, Nq, cap, n_prefix, D, fmt,
+                                1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0)
+    if workspace is None:
+        workspace = q.new_empty((nbytes,), dtype=torch.uint8)
+    else:
+        if workspace.get_device() != index:
+            raise ValueError(f"all tensors must be on one device: got {q.device} and {workspace.device}")
+        nbytes = workspace.numel() * workspace.element_size()
+    st = _cache_lib().fa_decode_cache(ctypes.byref(shp), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
+                                      lens.data_ptr(), pk, pv, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
+                                      nbytes, raw_stream(index))
     if st != FA_OK:
         raise FAError(st, "fa_decode_cache")
     return out, lse

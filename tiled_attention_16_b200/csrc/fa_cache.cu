@@ -83,6 +83,12 @@ __device__ __forceinline__ uint2 codes_int8(const uint4& w, uint32_t amax, float
     return make_uint2(c[0], c[1]);
 }
 
+// A CTA writes a tile of (rows / heads) tokens x heads of one sequence, heads
+// fastest.  heads is 1 where the tokens of a head follow one another in memory
+// (reads and writes of a tile are one run each); rows from a projection lie
+// token by token with the heads inside, and there tiles of four heads read
+// 1 KB and write 2 KB runs (one head a tile, 256 bytes apart: 4.1 TB/s against
+// 5.6 at 8 sequences of 2048 tokens and 32 heads of 128).
 template <int D, int kFmt>
 __global__ void __launch_bounds__(kCacheThreads)
 fa_cache_write_kernel(const CacheWriteParams p) {
@@ -92,24 +98,28 @@ fa_cache_write_kernel(const CacheWriteParams p) {
     const RopeRows& x = blockIdx.y ? p.v : p.k;
     uint8_t* cache = static_cast<uint8_t*>(blockIdx.y ? p.v_cache : p.k_cache);
     float* scales = blockIdx.y ? p.v_scale : p.k_scale;
-    const long long first = static_cast<long long>(blockIdx.x) * (kSlots * kRows) + threadIdx.x / kLanes;
+    const int shift = blockIdx.y ? p.v_shift : p.k_shift;   // log2 of the tile's heads
+    const unsigned n_tiles = (static_cast<unsigned>(p.N) + (kSlots * kRows >> shift) - 1) / (kSlots * kRows >> shift);
+    const unsigned h_tiles = (static_cast<unsigned>(p.H) + (1u << shift) - 1) >> shift;
+    const unsigned per = n_tiles * h_tiles;
+    const unsigned b = blockIdx.x / per, in = blockIdx.x - b * per;
+    if (b >= static_cast<unsigned>(p.B)) return;            // the other tensor has more tiles
+    const unsigned n0 = in / h_tiles * (kSlots * kRows >> shift), h0 = (in % h_tiles) << shift;
+    const long long start = __ldg(p.start + b);
+    const int cnt = p.count ? min(__ldg(p.count + b), p.N) : p.N;
     uint4 raw[kRows];
     long long slot[kRows];   // row of the cache, -1: not written
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const long long row = first + i * kSlots;
+        const int r = static_cast<int>(threadIdx.x / kLanes) + i * kSlots;
+        const int n = static_cast<int>(n0) + (r >> shift), h = static_cast<int>(h0) + (r & ((1 << shift) - 1));
+        const long long to = start + n;
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
         slot[i] = -1;
-        if (row < p.rows) {
-            const unsigned bh = static_cast<unsigned>(row) / static_cast<unsigned>(p.N);
-            const int n = static_cast<int>(static_cast<unsigned>(row) - bh * static_cast<unsigned>(p.N));
-            const int b = static_cast<int>(bh / static_cast<unsigned>(p.H));
-            const int h = static_cast<int>(bh - static_cast<unsigned>(b) * static_cast<unsigned>(p.H));
+        if (n < cnt && h < p.H && to >= 0 && to < p.capacity) {
+            slot[i] = (static_cast<long long>(b) * p.H + h) * p.capacity + to;
             raw[i] = __ldg(reinterpret_cast<const uint4*>(x.data + b * x.stride_b + h * x.stride_h + n * x.stride_n) +
                            lane);
-            const long long at = static_cast<long long>(__ldg(p.start + b)) + n;
-            const int cnt = p.count ? __ldg(p.count + b) : p.N;
-            if (n < cnt && at >= 0 && at < p.capacity) slot[i] = static_cast<long long>(bh) * p.capacity + at;
         }
     }
 #pragma unroll
@@ -211,10 +221,20 @@ dim3 cache_grid(int D, long long rows) {
 
 }  // namespace
 
-cudaError_t launch_cache_write(int D, int fmt, const CacheWriteParams& p, cudaStream_t stream) {
+cudaError_t launch_cache_write(int D, int fmt, CacheWriteParams p, cudaStream_t stream) {
+    const int rows = kCacheThreads / (D / 8) * kRows;
+    // Heads of a tile: four for rows that lie token by token; and when there are
+    // fewer tokens than rows, as many as fill the tile.
+    auto tiling = [&](const RopeRows& x, int& shift) {
+        shift = p.H > 1 && p.N > 1 && x.stride_h < x.stride_n ? 2 : 0;
+        while ((rows >> shift) / 2 >= p.N && (1 << shift) < p.H) ++shift;
+        const long long tn = rows >> shift, th = 1LL << shift;
+        return p.B * ((p.N + tn - 1) / tn) * ((p.H + th - 1) / th);
+    };
+    const long long tk = tiling(p.k, p.k_shift), tv = tiling(p.v, p.v_shift);
+    const dim3 grid(static_cast<unsigned>(tk > tv ? tk : tv), 2);
     return cache_dispatch(D, fmt, [&](auto d, auto f) {
-        fa_cache_write_kernel<decltype(d)::value, decltype(f)::value>
-            <<<cache_grid(D, p.rows), kCacheThreads, 0, stream>>>(p);
+        fa_cache_write_kernel<decltype(d)::value, decltype(f)::value><<<grid, kCacheThreads, 0, stream>>>(p);
         return cudaGetLastError();
     });
 }

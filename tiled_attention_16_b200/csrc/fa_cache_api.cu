@@ -245,10 +245,10 @@ fa_status fa_cache_write(const fa_cache_shape* shape, int N, const fa_rows* k, c
     p.v_cache = v_cache;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.B = s.B;
     p.H = s.Hkv;
     p.N = N;
     p.capacity = s.capacity;
-    p.rows = static_cast<long long>(s.B) * s.Hkv * N;
     return status_of(launch_cache_write(s.D, s.format, p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -20,9 +20,13 @@
 // by a power of two for each row (its largest value in [2^14, 2^15), values
 // below 2^-29 of that lose bits), the K scale multiplies S in fp32, and the V
 // scale goes into P.  P, times the V scale over a power of two that bounds the
-// scales seen so far, is rounded to fp16 with its row maximum at 2^14 (a value
-// of 2^-28 of the maximum is still a normal number: relative error 2^-11); the
-// row sum l is taken before that.  With bf16 caches P is rounded to bf16 (2^-8).
+// scales seen so far, is rounded to fp16 with its row maximum between 2^6 and
+// 2^14 (a value of 2^-20 of the maximum is still a normal number: relative
+// error 2^-11; below, the absolute one is 2^-31 of it); the row sum l is taken
+// before that.  With bf16 caches P is rounded to bf16 (2^-8).  The maximum in
+// use is replaced only when a score exceeds it by more than 8 (log2 units), and
+// the bound on the V scales when one exceeds it, so most tiles need one vote
+// and no shuffles or rescaling.
 //
 // The order of the contraction is free, so a lane reads 16 consecutive codes
 // of a key with one shared-memory load and uses them as its four k-steps; for
@@ -33,7 +37,6 @@
 
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
-#include <cuda_fp8.h>
 
 namespace fa {
 
@@ -42,6 +45,7 @@ namespace {
 constexpr int kCdThreads = 160;   // 4 compute warps + 1 producer warp
 constexpr int kCdKeys = 64;       // keys per tile
 constexpr float kLn2 = 0.69314718055994531f;
+constexpr float kCdRescale = 8.f; // growth of a row's maximum (log2 units) up to which the old one stays in use
 
 enum CdSite { kCdSiteFull = 20, kCdSiteEmpty = 21, kCdSiteDrain = 22 };
 
@@ -50,7 +54,10 @@ struct CdLayout {
     static constexpr int kElem = kFmt == 0 ? 2 : 1;
     static constexpr int kTileBytes = kCdKeys * D * kElem;              // one K or V tile
     static constexpr int kScaleBytes = kFmt == 0 ? 0 : kCdKeys * 4;
-    static constexpr int kStages = kFmt == 0 ? (D == 128 ? 3 : 4) : (D == 128 ? 4 : 6);
+    static constexpr int kStages = kFmt == 0 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
+    // CTAs an SM holds at once, by shared memory and by registers (five warps
+    // of at most 128 registers three times, of 168 twice)
+    static constexpr int kCtas(int nt) { return kFmt == 0 && D == 128 ? 2 : (nt == 1 ? 3 : 2); }
     static constexpr int kK = 0;
     static constexpr int kV = kStages * kTileBytes;
     static constexpr int kScales = 2 * kStages * kTileBytes;            // K then V scales of each stage
@@ -117,10 +124,11 @@ __device__ __forceinline__ void mma16(float (&c)[4], uint32_t a0, uint32_t a1, u
 template <int kFmt>
 __device__ __forceinline__ void unpack4(uint32_t c, uint32_t& lo, uint32_t& hi) {
     if constexpr (kFmt == 1) {
-        const __half2_raw a = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c & 0xffffu), __NV_E4M3);
-        const __half2_raw b = __nv_cvt_fp8x2_to_halfraw2(static_cast<__nv_fp8x2_storage_t>(c >> 16), __NV_E4M3);
-        lo = a.x | (static_cast<uint32_t>(a.y) << 16);
-        hi = b.x | (static_cast<uint32_t>(b.y) << 16);
+        asm("{\n\t.reg .b16 a, b;\n\t"
+            "mov.b32 {a, b}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, a;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+            : "=r"(lo), "=r"(hi) : "r"(c));
     } else {
         const uint32_t u = c ^ 0x80808080u;
         const __half2 off = __half2half2(__ushort_as_half(0x6480));   // 1152
@@ -233,14 +241,14 @@ __device__ __forceinline__ void cd_drain(uint64_t* bar, uint32_t parity) {
 
 // NT: blocks of 8 query rows a CTA holds.
 template <int D, int kFmt, int NT>
-__global__ void __launch_bounds__(kCdThreads)
+__global__ void __launch_bounds__(kCdThreads, CdLayout<D, kFmt>::kCtas(NT))
 fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const CacheDecodeParams p) {
     using L = CdLayout<D, kFmt>;
     constexpr bool kHalf = kFmt != 0;
     constexpr int kStages = L::kStages;
     constexpr int kSteps = D / 16;
-    constexpr float kShift = kHalf ? 14.f : 0.f;
+    constexpr float kShift = kHalf ? 6.f : 0.f;   // P is 2^kShift where the score is the row's (stale) maximum
     extern __shared__ uint8_t smem_raw[];
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
@@ -311,6 +319,8 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     Walk w = run.w;
     long long unit_at = run.unit_at;
     bool ok = true;
+    int st = 0;            // ring stage and its parity
+    uint32_t phase = 0u;
 
     // After a wait that gave up, the remaining units are walked without loads
     // or outputs, so that the barriers below stay matched.
@@ -374,29 +384,45 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         if (p.causal) pos_min = w.len - p.Nq;
 
         float o[NT][kSteps][4];
-        float m_run[NT][2], l_run[NT][2];
+        // stale row maximum, kShift less it (infinite before the first key), partial row sum
+        float m_run[NT][2], nm[NT][2], l_run[NT][2];
         float v_top = __int_as_float(1 << 23);   // power of two that bounds the V scales so far
+        float v_inv = pow2_inverse(v_top);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
             m_run[n][0] = m_run[n][1] = -INFINITY;
+            nm[n][0] = nm[n][1] = INFINITY;
             l_run[n][0] = l_run[n][1] = 0.f;
         }
 
         for (int i = 0; i < n_here; ++i, ++t) {
-            const int st = t % kStages;
-            ok = ok && mbar_wait(&full[st], (t / kStages) & 1, abort_flag, kCdSiteFull);
+            ok = ok && mbar_wait(&full[st], phase, abort_flag, kCdSiteFull);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) continue;
             const uint32_t kb = sK + st * L::kTileBytes, vb = sV + st * L::kTileBytes;
             const int key0 = (w.tile + i) * kCdKeys + kw;    // slot of the warp's first key
             const int kA = key0 + g8, kB = kA + 8;           // this lane's two keys in S^T
+            const bool edge = key0 + 15 > pos_min;           // some key is hidden from some row (warp-uniform)
+            const bool clear = key0 + 15 >= w.len;           // some key is behind the length
+            if (clear) {
+                // V rows behind the length may hold NaN, and 0 x NaN is NaN
+                constexpr int kChunks = D * L::kElem / 16;
+                for (int e = lane; e < 16 * kChunks; e += 32) {
+                    const int row = kw + e / kChunks;
+                    if (key0 + e / kChunks >= w.len)
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
+                                     ::"r"(vb + chunk_off<D, kFmt>(row, e % kChunks)), "r"(0u) : "memory");
+                }
+                __syncwarp();
+            }
             // ---- S^T (16 keys x rows) = K Q^T
             float s[NT][4];
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
             float ksA = 1.f, ksB = 1.f, vsA = 1.f, vsB = 1.f;
+            const int mi = lane >> 3;
             if constexpr (kHalf) {
                 const uint32_t sc = sS + st * 2 * L::kScaleBytes + (kw + g8) * 4;
                 ksA = lds32(sc);
@@ -420,8 +446,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     }
                 }
             } else {
-                const int mi = lane >> 3;                    // (keys lo, hi) x (d lo, hi)
-                const int krow = kw + (mi & 1) * 8 + (lane & 7);
+                const int krow = kw + (mi & 1) * 8 + (lane & 7);   // matrices: (keys lo, hi) x (d lo, hi)
 #pragma unroll
                 for (int kk = 0; kk < kSteps; ++kk) {
                     uint32_t a[4];
@@ -430,65 +455,53 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     for (int n = 0; n < NT; ++n) mma16<false>(s[n], a[0], a[1], a[2], a[3], qb[n][kk][0], qb[n][kk][1]);
                 }
             }
-            // ---- mask, online softmax (rows 2 t4, 2 t4 + 1; keys kA, kB)
-            const bool edge = key0 + 15 > pos_min;           // some key is hidden from some row (warp-uniform)
-            const bool inA = kA < w.len, inB = kB < w.len;
-            float vfac = 1.f;                                // what the V exponent's growth costs O
-            if constexpr (kHalf) {
-                float vm = fmaxf(inA ? vsA : 0.f, inB ? vsB : 0.f);
+            // ---- mask, online softmax (rows 2 t4, 2 t4 + 1; keys kA, kB).  Element e is
+            // (key e / 2, row e % 2); y = score + kShift - stale maximum, in log2 units.
+            float y[NT][4];
+            bool grow = false;
 #pragma unroll
-                for (int k = 4; k <= 16; k <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
-                const float top = fmaxf(v_top, pow2_at_least(vm));
-                const float inv = pow2_inverse(top);
-                vfac = v_top * inv;
-                v_top = top;
-                vsA *= inv;
-                vsB *= inv;
-            }
-            uint32_t pb[NT][2];
-#pragma unroll
-            for (int n = 0; n < NT; ++n) {
-                float x[4];   // (kA, row 0), (kA, row 1), (kB, row 0), (kB, row 1)
-                float mx[2], alpha[2];
+            for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    x[e] = s[n][e] * ((e >> 1) ? ksB : ksA) * qc[n][e & 1];
-                    if (edge && ((e >> 1) ? kB : kA) > pos[n][e & 1]) x[e] = -INFINITY;
+                    y[n][e] = fmaf(s[n][e], ((e >> 1) ? ksB : ksA) * qc[n][e & 1], nm[n][e & 1]);
+                    if (edge && ((e >> 1) ? kB : kA) > pos[n][e & 1]) y[n][e] = -INFINITY;
+                    grow |= y[n][e] > kShift + kCdRescale;
                 }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    mx[h] = fmaxf(x[h], x[2 + h]);
-#pragma unroll
-                    for (int k = 4; k <= 16; k <<= 1) mx[h] = fmaxf(mx[h], __shfl_xor_sync(0xffffffffu, mx[h], k));
-                    const float m_new = fmaxf(m_run[n][h], mx[h]);
-                    alpha[h] = m_new == -INFINITY ? 1.f : ex2(m_run[n][h] - m_new);
-                    m_run[n][h] = m_new;
-                }
-                float pw[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int h = e & 1;
-                    pw[e] = x[e] == -INFINITY ? 0.f : ex2(x[e] - m_run[n][h] + kShift);   // NaN stays NaN
-                }
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    l_run[n][h] = l_run[n][h] * alpha[h] + (pw[h] + pw[2 + h]);
-                    alpha[h] *= vfac;
-                }
+            if constexpr (kHalf) grow |= (vsA > v_top && kA < w.len) || (vsB > v_top && kB < w.len);
+            if (__any_sync(0xffffffffu, grow)) {
+                // a maximum grew by more than kCdRescale, or a V scale past the
+                // bound: take the new ones and bring the sums so far to them
+                float vfac = 1.f;
                 if constexpr (kHalf) {
+                    float vm = fmaxf(kA < w.len ? vsA : 0.f, kB < w.len ? vsB : 0.f);
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        // a masked key's scale may be anything
-                        const bool seen = !edge || ((e >> 1) ? kB : kA) <= pos[n][e & 1];
-                        pw[e] = seen ? pw[e] * ((e >> 1) ? vsB : vsA) : 0.f;
-                    }
-                    pb[n][0] = turn8x8(pack_half2(pw[0], pw[1]));
-                    pb[n][1] = turn8x8(pack_half2(pw[2], pw[3]));
-                } else {
-                    pb[n][0] = turn8x8(pack_bf16x2(pw[0], pw[1]));
-                    pb[n][1] = turn8x8(pack_bf16x2(pw[2], pw[3]));
+                    for (int k = 4; k <= 16; k <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
+                    const float top = fmaxf(v_top, pow2_at_least(vm));
+                    v_inv = pow2_inverse(top);
+                    vfac = v_top * v_inv;
+                    v_top = top;
                 }
-                if (__any_sync(0xffffffffu, alpha[0] != 1.f || alpha[1] != 1.f)) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float alpha[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const float xa = y[n][h] == -INFINITY ? -INFINITY : s[n][h] * (ksA * qc[n][h]);
+                        const float xb = y[n][2 + h] == -INFINITY ? -INFINITY : s[n][2 + h] * (ksB * qc[n][h]);
+                        float mx = fmaxf(xa, xb);
+#pragma unroll
+                        for (int k = 4; k <= 16; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
+                        const float m_new = fmaxf(m_run[n][h], mx);
+                        alpha[h] = m_new == -INFINITY ? 1.f : ex2(m_run[n][h] - m_new);
+                        m_run[n][h] = m_new;
+                        nm[n][h] = kShift - m_new;
+                        l_run[n][h] *= alpha[h];
+                        alpha[h] *= vfac;
+                        y[n][h] = xa + nm[n][h];            // -inf + inf, where no key was seen yet:
+                        y[n][2 + h] = xb + nm[n][h];        // put right below
+                        if (xa == -INFINITY) y[n][h] = -INFINITY;
+                        if (xb == -INFINITY) y[n][2 + h] = -INFINITY;
+                    }
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j) {
                         o[n][j][0] *= alpha[0];
@@ -498,14 +511,31 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     }
                 }
             }
-            // ---- O^T (D x rows) += V^T P^T; V rows behind the length are cleared
-            // (they may hold NaN, and 0 x NaN is NaN)
-            const int kv = key0 + 2 * t4;
-            const bool clear = key0 + 15 >= w.len;
-            const uint32_t one = kHalf ? 0x00ff00ffu : 0x0000ffffu;
-            const uint32_t mlo = clear ? (kv < w.len ? one : 0u) | (kv + 1 < w.len ? ~one : 0u) : 0xffffffffu;
-            const uint32_t mhi = clear ? (kv + 8 < w.len ? one : 0u) | (kv + 9 < w.len ? ~one : 0u) : 0xffffffffu;
-            const int mi = lane >> 3;
+            vsA *= v_inv;
+            vsB *= v_inv;
+            uint32_t pb[NT][2];
+#pragma unroll
+            for (int n = 0; n < NT; ++n) {
+                float pw[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) pw[e] = ex2(y[n][e]);
+                l_run[n][0] += pw[0] + pw[2];
+                l_run[n][1] += pw[1] + pw[3];
+                if constexpr (kHalf) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        pw[e] *= (e >> 1) ? vsB : vsA;
+                        // a hidden key's scale may be anything
+                        if (edge && y[n][e] == -INFINITY) pw[e] = 0.f;
+                    }
+                    pb[n][0] = turn8x8(pack_half2(pw[0], pw[1]));
+                    pb[n][1] = turn8x8(pack_half2(pw[2], pw[3]));
+                } else {
+                    pb[n][0] = turn8x8(pack_bf16x2(pw[0], pw[1]));
+                    pb[n][1] = turn8x8(pack_bf16x2(pw[2], pw[3]));
+                }
+            }
+            // ---- O^T (D x rows) += V^T P^T
             if constexpr (kHalf) {
                 // matrices: (keys lo, hi) x (chunk of 16 values j, j + 1)
                 const int vrow = kw + (mi & 1) * 8 + (lane & 7);
@@ -516,8 +546,8 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
                         uint32_t a0, a1, a2, a3;   // rows d = 16 j + 2 g8 (a0, a2) and + 1 (a1, a3)
-                        unpack4<kFmt>(__byte_perm(r[2 * u], 0u, 0x3120) & mlo, a0, a1);
-                        unpack4<kFmt>(__byte_perm(r[2 * u + 1], 0u, 0x3120) & mhi, a2, a3);
+                        unpack4<kFmt>(__byte_perm(r[2 * u], 0u, 0x3120), a0, a1);
+                        unpack4<kFmt>(__byte_perm(r[2 * u + 1], 0u, 0x3120), a2, a3);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16<true>(o[n][j + u], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                     }
@@ -530,12 +560,16 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     uint32_t r[4];
                     ldsm4_t(vb + chunk_off<D, kFmt>(vrow, 2 * j + (mi & 1)), r);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n)
-                        mma16<false>(o[n][j], r[0] & mlo, r[1] & mlo, r[2] & mhi, r[3] & mhi, pb[n][0], pb[n][1]);
+                    for (int n = 0; n < NT; ++n) mma16<false>(o[n][j], r[0], r[1], r[2], r[3], pb[n][0], pb[n][1]);
                 }
             }
+            if (clear) fence_proxy_async_smem();   // the zeros before the next copy into this stage
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
+            if (++st == kStages) {
+                st = 0;
+                phase ^= 1u;
+            }
         }
 
         // ---- the four warps' parts of the unit, joined in shared memory
@@ -737,8 +771,8 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f) {
 template <int D, int kFmt, int NT>
 cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p, cudaStream_t stream) {
     auto kern = fa_cache_decode_kernel<D, kFmt, NT>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, CdLayout<D, kFmt>::kAlloc);
+    static SmemOptIn opt_in;
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(kern), CdLayout<D, kFmt>::kAlloc);
     if (e != cudaSuccess) return e;
     kern<<<p.n_cta, kCdThreads, CdLayout<D, kFmt>::kAlloc, stream>>>(tk, tv, p);
     return cudaGetLastError();
@@ -756,9 +790,9 @@ cudaError_t go_fmt(int fmt, const CUtensorMap& tk, const CUtensorMap& tv, const 
 }  // namespace
 
 int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta) {
-    (void)D;
-    (void)rows_cta;
-    return fmt == 0 ? 2 : 2;
+    const int nt = rows_cta / 8;
+    if (D == 128) return fmt == 0 ? CdLayout<128, 0>::kCtas(nt) : CdLayout<128, 1>::kCtas(nt);
+    return fmt == 0 ? CdLayout<64, 0>::kCtas(nt) : CdLayout<64, 1>::kCtas(nt);
 }
 
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,

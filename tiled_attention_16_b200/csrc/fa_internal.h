@@ -1,6 +1,7 @@
 // fa_internal.h — launch interface shared by the host API and the kernels.
 #pragma once
 
+#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
@@ -160,6 +161,22 @@ cudaError_t launch_lse_merge(int D, long long rows, const void* o_part, const fl
                              float* lse_acc, void* o_out, int first, cudaStream_t stream);
 cudaError_t launch_accumulate(long long n, const void* src, float* acc, void* out, int first, cudaStream_t stream);
 
+// Raises a kernel's dynamic shared memory limit, once per device (the call
+// costs about as much as half a launch).
+struct SmemOptIn {
+    std::atomic<bool> done[64] = {};
+    cudaError_t set(const void* kernel, int bytes) {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const bool known = dev >= 0 && dev < 64;
+        if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
+        return e;
+    }
+};
+
 // bf16 rows of D contiguous values, indexed [b, h, n] by strides in elements.
 struct RopeRows {
     __nv_bfloat16* data;
@@ -179,21 +196,21 @@ struct RopeParams {
     int Hq, Hkv, N, rot, weight_bf16;
     float eps;
     long long tokens;  // B * N
-    int token_slots, head_parts, n_items;   // filled by the launch
+    int token_slots, parts_q, parts_k, items_q, n_items;   // filled by the launch
 };
 int rope_bwd_ctas(int sms);
 cudaError_t launch_qk_norm_rope(int D, int interleaved, RopeParams p, int sms, cudaStream_t stream);
 cudaError_t launch_qk_norm_rope_bwd(int D, int interleaved, RopeParams p, float* dqw, float* dkw, int sms,
                                     cudaStream_t stream);
 
-// Cache writes and reads (fa_cache.cu); rows = B * H * N.
+// Cache writes and reads (fa_cache.cu).
 struct CacheWriteParams {
     RopeRows k, v;
     const int *start, *count;
     void *k_cache, *v_cache;
     float *k_scale, *v_scale;
-    int H, N, capacity;
-    long long rows;
+    int B, H, N, capacity;
+    int k_shift, v_shift;    // filled by the launch
 };
 struct CacheReadParams {
     const void *k_cache, *v_cache;
@@ -201,9 +218,9 @@ struct CacheReadParams {
     const int* lens;
     void *k_out, *v_out;
     int H, N, capacity;
-    long long rows;
+    long long rows;          // B * H * N
 };
-cudaError_t launch_cache_write(int D, int fmt, const CacheWriteParams& p, cudaStream_t stream);
+cudaError_t launch_cache_write(int D, int fmt, CacheWriteParams p, cudaStream_t stream);
 cudaError_t launch_cache_read(int D, int fmt, const CacheReadParams& p, cudaStream_t stream);
 
 // Decoding over a cache (fa_cache_decode.cu).

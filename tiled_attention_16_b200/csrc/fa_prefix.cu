@@ -376,8 +376,8 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
 template <int D, bool kRows2>
 cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& p, cudaStream_t stream) {
     auto kern = fa_prefix_kernel<D, kRows2>;
-    cudaError_t e =
-        cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PfLayout<D, kRows2>::kAlloc);
+    static SmemOptIn opt_in;
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(kern), PfLayout<D, kRows2>::kAlloc);
     if (e != cudaSuccess) return e;
     kern<<<p.n_cta, kPfThreads, PfLayout<D, kRows2>::kAlloc, stream>>>(tk, tv, p);
     return cudaGetLastError();

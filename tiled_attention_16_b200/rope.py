@@ -10,11 +10,13 @@ missing or the device is not a B200 the calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch
 
-from .attention import FA_OK, FAError, _check, _same_device, _stream_ptr, lib, symbols_in
+from ._args import on_device, raw_stream, want
+from .attention import FA_OK, FAError, lib, symbols_in
 
 HEADER_PATH = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "include", "fa_rope.h")
 
@@ -55,27 +57,24 @@ def declared_symbols() -> list[str]:
     return symbols_in(HEADER_PATH)
 
 
-def check_rows(t: torch.Tensor, name: str, shape) -> FaRows:
-    """A bf16 CUDA view [B, H, N, D] whose rows of D values are contiguous, as
-    the C side takes it (which checks alignment, strides and, for views that
-    are written, overlap)."""
+def check_rows(t: torch.Tensor, name: str, shape, first: torch.Tensor | None = None) -> FaRows:
+    """A bf16 CUDA view [B, H, N, D] whose rows of D values are contiguous, on
+    the device of `first`, as the C side takes it (which checks alignment,
+    strides and, for views that are written, overlap)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be on a CUDA device (no CPU path)")
     if t.dtype != torch.bfloat16:
         raise TypeError(f"{name} must be torch.bfloat16, got {t.dtype}")
-    if t.shape != torch.Size(shape):
+    if t.shape != shape:
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if first is not None and t.get_device() != first.get_device():
+        raise ValueError(f"all tensors must be on one device: got {first.device} and {t.device}")
     sb, sh, sn, sd = t.stride()
     if sd != 1:
         raise ValueError(f"{name} must have contiguous rows (last stride 1, got {sd})")
     return FaRows(t.data_ptr(), sb, sh, sn)
-
-
-def _token_major(like: torch.Tensor) -> torch.Tensor:
-    B, H, N, D = like.shape
-    return torch.empty((B, N, H, D), device=like.device, dtype=torch.bfloat16).transpose(1, 2)
 
 
 def _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
@@ -83,24 +82,21 @@ def _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
         raise ValueError("q and k must be [B, H, N, D]")
     B, Hq, N, D = q.shape
     Hkv = k.shape[1]
-    qr, kr = check_rows(q, "q", (B, Hq, N, D)), check_rows(k, "k", (B, Hkv, N, D))
+    qr, kr = check_rows(q, "q", (B, Hq, N, D)), check_rows(k, "k", (B, Hkv, N, D), q)
     wt = q_weight.dtype
-    if wt not in (torch.bfloat16, torch.float32):
+    if wt != torch.float32 and wt != torch.bfloat16:
         raise TypeError(f"q_weight must be torch.bfloat16 or torch.float32, got {wt}")
-    _check(q_weight, "q_weight", (D,), wt)
-    _check(k_weight, "k_weight", (D,), wt)
+    want(q_weight, "q_weight", (D,), wt, q)
+    want(k_weight, "k_weight", (D,), wt, q)
     rot = 0
     if inv_freq is not None:
         rot = 2 * inv_freq.numel()
-        _check(inv_freq, "inv_freq", (rot // 2,), torch.float32)
+        want(inv_freq, "inv_freq", (rot // 2,), torch.float32, q)
     if positions is not None:
-        _check(positions, "positions", (B, N), torch.int32)
-    shp = FaRopeShape(B, Hq, Hkv, N, D, rot, 1 if interleaved else 0, float(eps), 1 if wt == torch.bfloat16 else 0)
-    return shp, qr, kr
-
-
-def _ptr(t):
-    return None if t is None or t.numel() == 0 else t.data_ptr()
+        want(positions, "positions", (B, N), torch.int32, q)
+    return (FaRopeShape(B, Hq, Hkv, N, D, rot, 1 if interleaved else 0, eps, 1 if wt == torch.bfloat16 else 0), qr, kr,
+            q_weight.data_ptr(), k_weight.data_ptr(), inv_freq.data_ptr() if rot else None,
+            None if positions is None else positions.data_ptr())
 
 
 def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_weight: torch.Tensor,
@@ -112,16 +108,22 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
     rotate; None: no rotation).  positions: int32 [B,N], default 0 .. N-1.
     Pairs are (i, i + rotary_dim / 2), or (2i, 2i + 1) when interleaved.
     Returns contiguous (q_out, k_out), bf16."""
-    shp, qr, kr = _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
-    out_q = torch.empty(q.shape, device=q.device, dtype=torch.bfloat16) if out_q is None else out_q
-    out_k = torch.empty(k.shape, device=q.device, dtype=torch.bfloat16) if out_k is None else out_k
-    _check(out_q, "out_q", q.shape)
-    _check(out_k, "out_k", k.shape)
-    dev = _same_device(q, k, q_weight, k_weight, inv_freq, positions, out_q, out_k)
-    with torch.cuda.device(dev):
-        st = _rope_lib().fa_qk_norm_rope(ctypes.byref(shp), ctypes.byref(qr), ctypes.byref(kr), q_weight.data_ptr(),
-                                         k_weight.data_ptr(), _ptr(inv_freq), _ptr(positions), out_q.data_ptr(),
-                                         out_k.data_ptr(), _stream_ptr(dev))
+    shp, qr, kr, qw, kw, freq, pos = _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    if out_q is None:
+        out_q = q.new_empty(q.shape)
+    else:
+        want(out_q, "out_q", q.shape, torch.bfloat16, q)
+    if out_k is None:
+        out_k = q.new_empty(k.shape)
+    else:
+        want(out_k, "out_k", k.shape, torch.bfloat16, q)
+    index = q.get_device()
+    guard = on_device(index)
+    if guard is not None:
+        with guard:
+            return qk_norm_rope(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved, out_q, out_k)
+    st = _rope_lib().fa_qk_norm_rope(ctypes.byref(shp), ctypes.byref(qr), ctypes.byref(kr), qw, kw, freq, pos,
+                                     out_q.data_ptr(), out_k.data_ptr(), raw_stream(index))
     if st != FA_OK:
         raise FAError(st, "fa_qk_norm_rope")
     return out_q, out_k
@@ -137,28 +139,40 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     dk_weight): dq, dk bf16 [B,H,N,D] views, token-major in memory unless views
     are given (of a packed gradient, for instance); the weights' gradients
     fp32 [D], summed in a fixed order."""
-    shp, qr, kr = _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
-    _check(dq_out, "dq_out", q.shape)
-    _check(dk_out, "dk_out", k.shape)
-    dq = _token_major(q) if dq is None else dq
-    dk = _token_major(k) if dk is None else dk
-    dqr, dkr = check_rows(dq, "dq", q.shape), check_rows(dk, "dk", k.shape)
-    D = q.shape[3]
-    dqw, dkw = torch.empty((2, D), device=q.device, dtype=torch.float32).unbind(0)
-    dev = _same_device(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, dq, dk, workspace)
-    with torch.cuda.device(dev):
-        L = _rope_lib()
-        if workspace is None:
-            nbytes = int(L.fa_qk_norm_rope_bwd_workspace_bytes(ctypes.byref(shp)))
-            workspace = torch.empty(max(nbytes, 256), device=dev, dtype=torch.uint8)
-        st = L.fa_qk_norm_rope_bwd(ctypes.byref(shp), dq_out.data_ptr(), dk_out.data_ptr(), ctypes.byref(qr),
-                                   ctypes.byref(kr), q_weight.data_ptr(), k_weight.data_ptr(), _ptr(inv_freq),
-                                   _ptr(positions), ctypes.byref(dqr), ctypes.byref(dkr), dqw.data_ptr(),
-                                   dkw.data_ptr(), workspace.data_ptr(),
-                                   workspace.numel() * workspace.element_size(), _stream_ptr(dev))
+    shp, qr, kr, qw, kw, freq, pos = _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
+    want(dq_out, "dq_out", q.shape, torch.bfloat16, q)
+    want(dk_out, "dk_out", k.shape, torch.bfloat16, q)
+    B, Hq, N, D = q.shape
+    if dq is None:
+        dq = q.new_empty((B, N, Hq, D)).transpose(1, 2)
+    if dk is None:
+        dk = q.new_empty((B, N, k.shape[1], D)).transpose(1, 2)
+    dqr, dkr = check_rows(dq, "dq", q.shape, q), check_rows(dk, "dk", k.shape, q)
+    index = q.get_device()
+    guard = on_device(index)
+    if guard is not None:
+        with guard:
+            return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved,
+                                    dq, dk, workspace)
+    L = _rope_lib()
+    dqw, dkw = (q.new_empty((D,), dtype=torch.float32) for _ in range(2))
+    if workspace is None:
+        workspace = q.new_empty((_bwd_workspace(D, index),), dtype=torch.uint8)
+    elif workspace.get_device() != index:
+        raise ValueError(f"all tensors must be on one device: got {q.device} and {workspace.device}")
+    st = L.fa_qk_norm_rope_bwd(ctypes.byref(shp), dq_out.data_ptr(), dk_out.data_ptr(), ctypes.byref(qr),
+                               ctypes.byref(kr), qw, kw, freq, pos, ctypes.byref(dqr), ctypes.byref(dkr),
+                               dqw.data_ptr(), dkw.data_ptr(), workspace.data_ptr(),
+                               workspace.numel() * workspace.element_size(), raw_stream(index))
     if st != FA_OK:
         raise FAError(st, "fa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
+
+
+@functools.lru_cache(maxsize=None)
+def _bwd_workspace(D: int, index: int) -> int:
+    """At least 256, so that a refused head dimension is the library's to report."""
+    return max(qk_norm_rope_bwd_workspace_bytes(D), 256)
 
 
 def qk_norm_rope_bwd_workspace_bytes(D: int) -> int:
