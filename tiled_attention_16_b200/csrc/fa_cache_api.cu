@@ -117,7 +117,11 @@ fa_status check_decode(const fa_cache_decode_shape* s) {
     if (st != FA_OK && st != FA_ERR_UNSUPPORTED) return st;
     if (s->Hq < 1 || s->Nq < 1 || s->n_prefix < 0 || s->Hq % s->Hkv != 0) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return FA_ERR_INVALID_ARG;
-    if (static_cast<long long>(s->B) * s->Hq * s->Nq > (1LL << 24)) return FA_ERR_INVALID_ARG;
+    const long long rows = static_cast<long long>(s->B) * s->Hq * s->Nq;
+    if (rows > (1LL << 24)) return FA_ERR_INVALID_ARG;
+    // the kernels number the key tiles of all row blocks with 32 bits
+    if (rows * ((s->capacity + 63LL) / 64 + 8) > kIntMax || rows * ((s->n_prefix + 127LL) / 128) > kIntMax)
+        return FA_ERR_INVALID_ARG;
     return st;
 }
 
@@ -137,7 +141,7 @@ DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
     pl.RB = (R + pl.rows_cta - 1) / pl.rows_cta;
     const long long units = static_cast<long long>(s.B) * s.Hkv * pl.RB;
     const long long most = units * ((s.capacity + 63LL) / 64);
-    const long long resident = static_cast<long long>(sms) * cache_decode_ctas_per_sm(s.D, s.format, pl.rows_cta);
+    const long long resident = static_cast<long long>(sms) * cache_decode_ctas_per_sm(s.D, s.format);
     pl.n_cta = static_cast<int>(std::min(most, resident));
     const long long rows = static_cast<long long>(s.B) * s.Hq * s.Nq;
     if (s.n_prefix > 0) {
@@ -147,10 +151,16 @@ DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
         pl.subs = two ? 1 : 2;
         pl.n_rowtiles = static_cast<int>((head_rows + pl.rows_unit - 1) / pl.rows_unit);
         pl.n_tiles = (s.n_prefix + kTileN - 1) / kTileN;
-        const long long tiles = static_cast<long long>(s.Hkv) * pl.n_rowtiles * pl.n_tiles;
+        const long long units = static_cast<long long>(s.Hkv) * pl.n_rowtiles, tiles = units * pl.n_tiles;
         // alternating blocks want two key tiles a CTA
-        const long long want = two ? tiles : (tiles + 1) / 2;
-        pl.n_pcta = static_cast<int>(std::min<long long>(want, sms));
+        const long long most = std::min<long long>(two ? tiles : (tiles + 1) / 2, sms);
+        pl.n_pcta = static_cast<int>(most);
+        // A part costs about three key tiles besides its own (its Q, an empty
+        // pipeline, its results).  With a multiple of the units as CTAs each has
+        // one part; that is taken where it beats all SMs with two parts on most.
+        const long long even = most / units * units;
+        if (even > 0 && even < most && (tiles + even - 1) / even + 3 <= (tiles + most - 1) / most + 6)
+            pl.n_pcta = static_cast<int>(even);
     }
     size_t at = 0;
     auto take = [&](size_t bytes) {
@@ -328,6 +338,7 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
     p.RB = pl.RB;
     p.HR = s.Hkv * pl.RB;
     p.n_cta = pl.n_cta;
+    p.unit_cost = cache_decode_unit_cost(pl.rows_cta);
     p.scale_log2 = static_cast<float>(static_cast<double>(s.scale) * kLog2e);
     PrefixParams f{};
     f.n_cta = pl.n_pcta;
@@ -352,7 +363,7 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
         f.scale_log2 = p.scale_log2;
         e = launch_prefix(s.D, pk, pv, f, strm);
     }
-    if (e == cudaSuccess) e = launch_cache_decode(s.D, s.format, tk, tv, p, strm);
+    if (e == cudaSuccess) e = launch_cache_decode(s.D, s.format, tk, tv, p, s.n_prefix > 0, strm);
     if (e == cudaSuccess) e = launch_cache_combine(s.D, p, f, strm);
     return status_of(e);
 }

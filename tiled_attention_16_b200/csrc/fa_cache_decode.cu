@@ -49,24 +49,29 @@ constexpr float kCdRescale = 8.f; // growth of a row's maximum (log2 units) up t
 
 enum CdSite { kCdSiteFull = 20, kCdSiteEmpty = 21, kCdSiteDrain = 22 };
 
-template <int D, int kFmt>
+template <int D, int kFmt, int NT>
 struct CdLayout {
     static constexpr int kElem = kFmt == 0 ? 2 : 1;
-    static constexpr int kTileBytes = kCdKeys * D * kElem;              // one K or V tile
-    static constexpr int kScaleBytes = kFmt == 0 ? 0 : kCdKeys * 4;
-    static constexpr int kStages = kFmt == 0 ? (D == 128 ? 3 : 4) : (D == 128 ? 3 : 6);
+    static constexpr bool kWide = kFmt == 0 && D == 128;                // 32 KB a stage
     // CTAs an SM holds at once, by shared memory and by registers (five warps
     // of at most 128 registers three times, of 168 twice)
-    static constexpr int kCtas(int nt) { return kFmt == 0 && D == 128 ? 2 : (nt == 1 ? 3 : 2); }
+    static constexpr int kCtas = kWide ? 2 : 3;
+    static constexpr int kTileBytes = kCdKeys * D * kElem;              // one K or V tile
+    static constexpr int kScaleBytes = kFmt == 0 ? 0 : kCdKeys * 4;
+    static constexpr int kStages = D == 128 ? 3 : (kFmt == 0 ? 3 : 6);
+    static constexpr int kQFrag = NT * (D / 16) * 32 * 8;               // Q^T fragments of a unit
     static constexpr int kK = 0;
     static constexpr int kV = kStages * kTileBytes;
     static constexpr int kScales = 2 * kStages * kTileBytes;            // K then V scales of each stage
-    static constexpr int kMerge = kScales + 2 * kStages * kScaleBytes;  // [4 warps][8 rows][kCols + 4] fp32
-    static constexpr int kCols = 64;
+    static constexpr int kQ = kScales + 2 * kStages * kScaleBytes;      // two units' fragments,
+    static constexpr int kQScale = kQ + 2 * kQFrag;                     // and their rows' factors
+    static constexpr int kMerge = kQScale + 2 * NT * 8 * 4;             // [4 warps][8 rows][kCols + 4] fp32
+    static constexpr int kCols = kWide ? (NT == 1 ? 64 : 32) : (NT == 1 ? D : 64);
     static constexpr int kMl = kMerge + 4 * 8 * (kCols + 4) * 4;        // m, l and V exponent of the warps
     static constexpr int kBar = kMl + 4 * 40 * 4;
-    static constexpr int kBytes = kBar + 2 * kStages * 8 + 48;
+    static constexpr int kBytes = kBar + (2 * kStages + 4) * 8 + 16;
     static constexpr int kAlloc = kBytes + 1024;
+    static_assert((kAlloc + 1024) * kCtas <= 228 * 1024, "CTAs must fit");
 };
 
 // Byte offset of the 16-byte chunk `c` of key row `row` in a tile as TMA
@@ -76,6 +81,12 @@ template <int D, int kFmt>
 __device__ __forceinline__ uint32_t chunk_off(int row, int c) {
     if constexpr (kFmt != 0 && D == 64) return row * 64 + ((c ^ ((row >> 1) & 3)) << 4);
     return (c >> 3) * (kCdKeys * 128) + row * 128 + (((c & 7) ^ (row & 7)) << 4);
+}
+
+// The address `c` chunks on (c even, or the first chunk even) from an address
+// that chunk_off() gave.
+__device__ __forceinline__ uint32_t chunk_at(uint32_t addr, int c) {
+    return (addr ^ ((c & 7) << 4)) + (c >> 3) * (kCdKeys * 128);
 }
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
@@ -90,6 +101,11 @@ __device__ __forceinline__ uint4 lds128(uint32_t addr) {
     uint4 v;
     asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t addr) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr) : "memory");
     return v;
 }
 __device__ __forceinline__ float lds32(uint32_t addr) {
@@ -139,6 +155,21 @@ __device__ __forceinline__ void unpack4(uint32_t c, uint32_t& lo, uint32_t& hi) 
     }
 }
 
+// Four codes (d, d + 1 of a first key, then of a second) to fp16, by d.
+template <int kFmt>
+__device__ __forceinline__ void unpack4_pairs(uint32_t c, uint32_t& d0, uint32_t& d1) {
+    if constexpr (kFmt == 1) {
+        unpack4<1>(__byte_perm(c, 0u, 0x3120), d0, d1);
+    } else {
+        const uint32_t u = c ^ 0x80808080u;
+        const __half2 off = __half2half2(__ushort_as_half(0x6480));
+        uint32_t a = __byte_perm(u, 0x64646464u, 0x4240), b = __byte_perm(u, 0x64646464u, 0x4341);
+        __half2 ah = __hsub2(*reinterpret_cast<__half2*>(&a), off), bh = __hsub2(*reinterpret_cast<__half2*>(&b), off);
+        d0 = *reinterpret_cast<uint32_t*>(&ah);
+        d1 = *reinterpret_cast<uint32_t*>(&bh);
+    }
+}
+
 __device__ __forceinline__ uint32_t pack_half2(float lo, float hi) {
     const __half2 h = __floats2half2_rn(lo, hi);
     return *reinterpret_cast<const uint32_t*>(&h);
@@ -161,16 +192,34 @@ __device__ __forceinline__ int seq_tiles(const CacheDecodeParams& p, int b) {
     return max(1, (seq_len(p, b) + kCdKeys - 1) / kCdKeys);
 }
 
-// A CTA's place in the run of tiles: tile `tile` of unit (b, hr), hr = K/V
-// head * row blocks + row block.
+// Work is dealt out by position: a unit (sequence b; hr = K/V head * row blocks
+// + row block) covers unit_cost positions for what it costs besides its tiles,
+// then one for each tile.  All units lie end to end and CTA c of n takes
+// positions [total c / n, total (c + 1) / n).
 struct Walk {
-    int b, hr, tile, tiles, len;
+    int x0, x1, total, n;       // the CTA's positions, all positions, CTAs with any
+    int b, hr, at, tiles, len;  // unit, its first position, its tiles, its sequence's length
+    int t0, t1;                 // the CTA's tiles of it
+
     __device__ __forceinline__ void enter(const CacheDecodeParams& p) {
         len = seq_len(p, b);
         tiles = max(1, (len + kCdKeys - 1) / kCdKeys);
     }
-    __device__ __forceinline__ void next_unit(const CacheDecodeParams& p) {
-        tile = 0;
+    __device__ __forceinline__ void clip(const CacheDecodeParams& p) {
+        t0 = max(0, x0 - at - p.unit_cost);
+        t1 = min(tiles, x1 - at - p.unit_cost);
+    }
+    // to the first unit from here on that the CTA has tiles of; false: none
+    __device__ __forceinline__ bool settle(const CacheDecodeParams& p) {
+        while (at < x1) {
+            clip(p);
+            if (t0 < t1) return true;
+            step(p);
+        }
+        return false;
+    }
+    __device__ __forceinline__ void step(const CacheDecodeParams& p) {
+        at += tiles + p.unit_cost;
         if (++hr == p.HR) {
             hr = 0;
             ++b;
@@ -179,52 +228,41 @@ struct Walk {
     }
 };
 
-struct RunStart {
-    long long x0, x1, unit_at, total;   // the CTA's tiles, where its first unit starts, all tiles
-    int n;                              // CTAs with a run: no more than there are tiles
+// Warp-wide: CTA c of n, at the unit its positions begin in.
+__device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int n, int lane) {
     Walk w;
-};
-
-// Warp-wide: the run of CTA c of n (none for those past the number of tiles,
-// so that the CTAs that share a unit are consecutive).
-__device__ __forceinline__ RunStart find_run(const CacheDecodeParams& p, int c, int n, int lane) {
-    RunStart s;
-    long long total = 0;
-    for (int b0 = 0; b0 < p.B; b0 += 32) {
-        long long v = b0 + lane < p.B ? static_cast<long long>(seq_tiles(p, b0 + lane)) * p.HR : 0;
-        for (int k = 16; k; k >>= 1) v += __shfl_xor_sync(0xffffffffu, v, k);
-        total += v;
-    }
-    if (n > total) n = static_cast<int>(total);
-    s.n = n;
-    s.total = total;
-    s.x0 = c < n ? total * c / n : 0;
-    s.x1 = c < n ? total * (c + 1) / n : 0;
-    s.w = Walk{0, 0, 0, 1, 0};
-    s.unit_at = 0;
-    long long at = 0;
-    for (int b0 = 0; b0 < p.B && s.x0 < s.x1; b0 += 32) {
-        const long long v = b0 + lane < p.B ? static_cast<long long>(seq_tiles(p, b0 + lane)) * p.HR : 0;
-        long long incl = v;
+    int total = 0;
+#pragma unroll 4
+    for (int b = lane; b < p.B; b += 32) total += (seq_tiles(p, b) + p.unit_cost) * p.HR;
+    total = __reduce_add_sync(0xffffffffu, total);
+    n = min(n, total);          // every CTA has a position, so those that share a unit are consecutive
+    w.n = n;
+    w.total = total;
+    w.x0 = c < n ? static_cast<int>(static_cast<long long>(total) * c / n) : 0;
+    w.x1 = c < n ? static_cast<int>(static_cast<long long>(total) * (c + 1) / n) : 0;
+    w.b = w.hr = w.at = w.len = w.t0 = w.t1 = 0;
+    w.tiles = 1;
+    int at = 0;
+    for (int b0 = 0; b0 < p.B && w.x0 < w.x1; b0 += 32) {
+        const int v = b0 + lane < p.B ? (seq_tiles(p, b0 + lane) + p.unit_cost) * p.HR : 0;
+        int incl = v;
         for (int k = 1; k < 32; k <<= 1) {
-            const long long o = __shfl_up_sync(0xffffffffu, incl, k);
+            const int o = __shfl_up_sync(0xffffffffu, incl, k);
             if (lane >= k) incl += o;
         }
-        const unsigned past = __ballot_sync(0xffffffffu, at + incl > s.x0);
+        const unsigned past = __ballot_sync(0xffffffffu, at + incl > w.x0);
         if (past) {
             const int src = __ffs(past) - 1;
-            const long long seq_at = __shfl_sync(0xffffffffu, at + incl - v, src);
-            s.w.b = b0 + src;
-            s.w.enter(p);
-            const long long off = s.x0 - seq_at;
-            s.w.hr = static_cast<int>(off / s.w.tiles);
-            s.w.tile = static_cast<int>(off - static_cast<long long>(s.w.hr) * s.w.tiles);
-            s.unit_at = s.x0 - s.w.tile;
+            w.at = __shfl_sync(0xffffffffu, at + incl - v, src);
+            w.b = b0 + src;
+            w.enter(p);
+            w.hr = (w.x0 - w.at) / (w.tiles + p.unit_cost);
+            w.at += w.hr * (w.tiles + p.unit_cost);
             break;
         }
         at += __shfl_sync(0xffffffffu, incl, 31);
     }
-    return s;
+    return w;
 }
 
 __device__ __forceinline__ void cd_drain(uint64_t* bar, uint32_t parity) {
@@ -239,12 +277,61 @@ __device__ __forceinline__ void cd_drain(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// One warp: the B fragments of Q^T for rows row0 .. row0 + 8 NT - 1 of the K/V
+// head whose rows start at rows_at, in the order the MMAs take them (fragment
+// (n, step): 8 bytes a lane), and the rows' factors from the products to
+// log2-unit scores.  Rows past the head's are zero.
+template <int D, int kFmt, int NT>
+__device__ __forceinline__ void q_fragments(const CacheDecodeParams& p, uint8_t* smem, int buf, size_t rows_at, int row0,
+                                            int lane) {
+    using L = CdLayout<D, kFmt, NT>;
+    constexpr int kSteps = D / 16;
+    const int g8 = lane >> 2, t4 = lane & 3, R = p.G * p.Nq;
+    uint2* frag = reinterpret_cast<uint2*>(smem + L::kQ + buf * L::kQFrag) + lane;
+    float* factor = reinterpret_cast<float*>(smem + L::kQScale) + buf * NT * 8;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int r = row0 + n * 8 + g8;
+        const __nv_bfloat16* qrow = reinterpret_cast<const __nv_bfloat16*>(p.q) + (rows_at + (r < R ? r : 0)) * D;
+        if constexpr (kFmt != 0) {
+            uint2 raw[kSteps];
+            uint32_t am = 0u;
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                // step s = 4 hh + w4: values (chunk of 16) * 16 + 4 w4 .. + 3
+                const int d = (D == 128 ? (2 * t4 + (s >> 2)) : t4) * 16 + (s & 3) * 4;
+                raw[s] = r < R ? __ldg(reinterpret_cast<const uint2*>(qrow + d)) : make_uint2(0u, 0u);
+                am = __vmaxu2(am, __vmaxu2(raw[s].x & 0x7fff7fffu, raw[s].y & 0x7fff7fffu));
+            }
+            am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 1));
+            am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 2));
+            // 2^(14 - exponent of the row's largest value); q = 0: any
+            const int ex = static_cast<int>(max(am & 0xffffu, am >> 16) >> 7) - 127;
+            const int f = min(max(14 - ex, -113), 126);
+            const float up = __int_as_float((127 + f) << 23);
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s)
+                frag[(n * kSteps + s) * 32] =
+                    make_uint2(pack_half2(__uint_as_float(raw[s].x << 16) * up, __uint_as_float(raw[s].x & 0xffff0000u) * up),
+                               pack_half2(__uint_as_float(raw[s].y << 16) * up, __uint_as_float(raw[s].y & 0xffff0000u) * up));
+            if (t4 == 0) factor[n * 8 + g8] = pow2_inverse(up) * p.scale_log2;
+        } else {
+#pragma unroll
+            for (int s = 0; s < kSteps; ++s) {
+                const uint32_t* at = reinterpret_cast<const uint32_t*>(qrow + s * 16 + 2 * t4);
+                frag[(n * kSteps + s) * 32] = r < R ? make_uint2(__ldg(at), __ldg(at + 4)) : make_uint2(0u, 0u);
+            }
+            if (t4 == 0) factor[n * 8 + g8] = p.scale_log2;
+        }
+    }
+}
+
 // NT: blocks of 8 query rows a CTA holds.
 template <int D, int kFmt, int NT>
-__global__ void __launch_bounds__(kCdThreads, CdLayout<D, kFmt>::kCtas(NT))
+__global__ void __launch_bounds__(kCdThreads, CdLayout<D, kFmt, NT>::kCtas)
 fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const CacheDecodeParams p) {
-    using L = CdLayout<D, kFmt>;
+    using L = CdLayout<D, kFmt, NT>;
     constexpr bool kHalf = kFmt != 0;
     constexpr int kStages = L::kStages;
     constexpr int kSteps = D / 16;
@@ -253,7 +340,9 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
     uint64_t* empty = full + kStages;
-    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kBar + 2 * kStages * 8);
+    uint64_t* q_full = empty + kStages;    // [2]
+    uint64_t* q_empty = q_full + 2;        // [2]
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kBar + (2 * kStages + 4) * 8);
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
@@ -262,50 +351,76 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], 4);
         }
+        for (int s = 0; s < 2; ++s) {
+            mbar_init(&q_full[s], 32);
+            mbar_init(&q_empty[s], 4);
+        }
         *abort_flag = 0;
         fence_mbar_init();
     }
-    const RunStart run = find_run(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), lane);
+    grid_launch_dependents();
+    Walk w = find_run(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), lane);
+    bool more = w.settle(p);
     __syncthreads();
-    const int n_run = static_cast<int>(run.x1 - run.x0);
-    if (n_run == 0) return;   // the whole CTA
 
     if (warp == 4) {
         // ------------------------------------------------------------ producer
         if (lane == 0) {
             tma_prefetch_desc(&tmK);
             tma_prefetch_desc(&tmV);
-            Walk w = run.w;
-            int issued = 0;
-            for (int t = 0; t < n_run; ++t) {
-                const int st = t % kStages;
-                if (t >= kStages && !mbar_wait(&empty[st], ((t / kStages) - 1) & 1, abort_flag, kCdSiteEmpty)) break;
-                const int key0 = w.tile * kCdKeys;
-                const int bkv = w.b * p.Hkv + w.hr / p.RB;
-                // the scales' rows end at the capacity, a multiple of 4
-                const uint32_t sbytes = kHalf ? static_cast<uint32_t>(min(kCdKeys, p.capacity - key0)) * 4u : 0u;
-                mbar_arrive_expect_tx(&full[st], 2 * L::kTileBytes + 2 * sbytes);
-                constexpr int kBox = D * L::kElem > 128 ? 2 : 1;
+        }
+        int issued = 0, unit = 0, st = 0;
+        uint32_t phase = 1u;               // the first pass over the ring waits for nothing
+        bool ok = true;
+        for (; more && ok; w.step(p), more = w.settle(p), ++unit) {
+            const int hkv = w.hr / p.RB, bkv = w.b * p.Hkv + hkv;
+            for (int i = w.t0; i < w.t1; ++i) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], phase, abort_flag, kCdSiteEmpty));
+                if (!ok) break;
+                if (lane == 0) {
+                    const int key0 = i * kCdKeys;
+                    // the scales' rows end at the capacity, a multiple of 4
+                    const uint32_t sbytes = kHalf ? static_cast<uint32_t>(min(kCdKeys, p.capacity - key0)) * 4u : 0u;
+                    mbar_arrive_expect_tx(&full[st], 2 * L::kTileBytes + 2 * sbytes);
+                    constexpr int kBox = D * L::kElem > 128 ? 2 : 1;
 #pragma unroll
-                for (int a = 0; a < kBox; ++a) {
-                    tma_load_3d(smem + L::kK + st * L::kTileBytes + a * (L::kTileBytes / kBox), &tmK, &full[st], a * 64,
-                                key0, bkv);
-                    tma_load_3d(smem + L::kV + st * L::kTileBytes + a * (L::kTileBytes / kBox), &tmV, &full[st], a * 64,
-                                key0, bkv);
+                    for (int a = 0; a < kBox; ++a)
+                        tma_load_3d(smem + L::kK + st * L::kTileBytes + a * (L::kTileBytes / kBox), &tmK, &full[st],
+                                    a * 64, key0, bkv);
+#pragma unroll
+                    for (int a = 0; a < kBox; ++a)
+                        tma_load_3d(smem + L::kV + st * L::kTileBytes + a * (L::kTileBytes / kBox), &tmV, &full[st],
+                                    a * 64, key0, bkv);
+                    if constexpr (kHalf) {
+                        const size_t at = static_cast<size_t>(bkv) * p.capacity + key0;
+                        bulk_load(smem + L::kScales + st * 2 * L::kScaleBytes, p.k_scale + at, sbytes, &full[st]);
+                        bulk_load(smem + L::kScales + st * 2 * L::kScaleBytes + L::kScaleBytes, p.v_scale + at, sbytes,
+                                  &full[st]);
+                    }
                 }
-                if constexpr (kHalf) {
-                    const size_t at = static_cast<size_t>(bkv) * p.capacity + key0;
-                    bulk_load(smem + L::kScales + st * 2 * L::kScaleBytes, p.k_scale + at, sbytes, &full[st]);
-                    bulk_load(smem + L::kScales + st * 2 * L::kScaleBytes + L::kScaleBytes, p.v_scale + at, sbytes,
-                              &full[st]);
+                __syncwarp();
+                ++issued;
+                if (++st == kStages) {
+                    st = 0;
+                    phase ^= 1u;
                 }
-                issued = t + 1;
-                if (++w.tile == w.tiles) w.next_unit(p);
+                if (i == w.t0) {
+                    // the unit's Q^T fragments, while its first tiles are under way
+                    const int buf = unit & 1;
+                    ok = __all_sync(0xffffffffu,
+                                    mbar_wait(&q_empty[buf], ((unit >> 1) & 1) ^ 1, abort_flag, kCdSiteEmpty));
+                    if (!ok) break;
+                    q_fragments<D, kFmt, NT>(p, smem, buf, static_cast<size_t>(bkv) * (p.G * p.Nq),
+                                             (w.hr - hkv * p.RB) * (8 * NT), lane);
+                    mbar_arrive(&q_full[buf]);
+                }
             }
-            // nothing may still be landing in shared memory when the CTA leaves
+        }
+        // nothing may still be landing in shared memory when the CTA leaves
+        if (lane == 0)
             for (int t = (issued > kStages ? issued - kStages : 0); t < issued; ++t)
                 cd_drain(&full[t % kStages], (t / kStages) & 1);
-        }
+        grid_wait();   // behind a prefix kernel: this one ends after it, as the combine expects
         return;
     }
 
@@ -313,74 +428,47 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     const int g8 = lane >> 2, t4 = lane & 3;
     const int kw = warp * 16;                       // this warp's 16 keys in a tile
     const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV), sS = smem_u32(smem + L::kScales);
+    const uint32_t sQ = smem_u32(smem + L::kQ), sQScale = smem_u32(smem + L::kQScale);
     float* merge = reinterpret_cast<float*>(smem + L::kMerge);
     float* ml = reinterpret_cast<float*>(smem + L::kMl);   // [warp]: m [16], l [16], V exponent
     const int R = p.G * p.Nq;
-    Walk w = run.w;
-    long long unit_at = run.unit_at;
+    // Where this lane reads in a K and in a V tile: the chunk of the first step;
+    // chunk_at() gives the others (tile bases are multiples of the swizzle).
+    //   8 bits  K: keys kw + g8 (+ 8), chunks 2 t4 + hh of 16 codes;
+    //           V: matrices (keys lo, hi) x (chunks j, j + 1)
+    //   bf16    K: matrices (keys lo, hi) x (d lo, hi);  V: (d lo, hi) x (keys lo, hi)
+    const int mi = lane >> 3;
+    const uint32_t k_at = kHalf ? chunk_off<D, kFmt>(kw + g8, D == 128 ? 2 * t4 : t4)
+                                : chunk_off<D, kFmt>(kw + (mi & 1) * 8 + (lane & 7), mi >> 1);
+    const uint32_t v_at = kHalf ? chunk_off<D, kFmt>(kw + (mi & 1) * 8 + (lane & 7), mi >> 1)
+                                : chunk_off<D, kFmt>(kw + (mi >> 1) * 8 + (lane & 7), mi & 1);
     bool ok = true;
+    int unit = 0;
     int st = 0;            // ring stage and its parity
     uint32_t phase = 0u;
 
     // After a wait that gave up, the remaining units are walked without loads
     // or outputs, so that the barriers below stay matched.
-    for (int t = 0; t < n_run;) {
-        // ---- one unit, or the part of it in this CTA's run
-        const int n_here = min(w.tiles - w.tile, n_run - t);
+    for (; more; w.step(p), more = w.settle(p)) {
+        // ---- one unit, or the CTA's part of it
         const int hkv = w.hr / p.RB;
         const int row0 = (w.hr - hkv * p.RB) * (8 * NT);
         const size_t rows_at = static_cast<size_t>(w.b * p.Hkv + hkv) * R;   // first query row of the K/V head
-        // Q^T fragments: query row n * 8 + g8; zero on rows past R
-        uint32_t qb[NT][kSteps][2];
-        float qc[NT][2];      // softmax scale (log2 units) over q's power of two, rows 2 t4, 2 t4 + 1
-        int pos[NT][2];       // last visible slot of rows 2 t4, 2 t4 + 1
+        const int buf = unit & 1;
+        ok = ok && mbar_wait(&q_full[buf], (unit >> 1) & 1, abort_flag, kCdSiteFull);
+        ok = __all_sync(0xffffffffu, ok);
+        const uint32_t qf = sQ + buf * L::kQFrag + lane * 8;
+        float qc[NT][2];      // factor to log2-unit scores, rows 2 t4, 2 t4 + 1
+        int pos[NT][2];       // their last visible slot
         int pos_min = w.len - 1;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            const int r = row0 + n * 8 + g8;
-            const __nv_bfloat16* qrow =
-                reinterpret_cast<const __nv_bfloat16*>(p.q) + (rows_at + (r < R ? r : 0)) * D;
-            if constexpr (kHalf) {
-                uint2 raw[kSteps];
-                uint32_t am = 0u;
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    // step s = 4 hh + w4: values (chunk of 16) * 16 + 4 w4 .. + 3
-                    const int d = (D == 128 ? (2 * t4 + (s >> 2)) : t4) * 16 + (s & 3) * 4;
-                    raw[s] = r < R ? __ldg(reinterpret_cast<const uint2*>(qrow + d)) : make_uint2(0u, 0u);
-                    am = __vmaxu2(am, __vmaxu2(raw[s].x & 0x7fff7fffu, raw[s].y & 0x7fff7fffu));
-                }
-                am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 1));
-                am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 2));
-                // 2^(14 - exponent of the row's largest value); q = 0: any
-                const int ex = static_cast<int>(max(am & 0xffffu, am >> 16) >> 7) - 127;
-                const int f = min(max(14 - ex, -113), 126);
-                const float up = __int_as_float((127 + f) << 23);
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s) {
-                    qb[n][s][0] = pack_half2(__uint_as_float(raw[s].x << 16) * up,
-                                             __uint_as_float(raw[s].x & 0xffff0000u) * up);
-                    qb[n][s][1] = pack_half2(__uint_as_float(raw[s].y << 16) * up,
-                                             __uint_as_float(raw[s].y & 0xffff0000u) * up);
-                }
-                const float back = pow2_inverse(up);
-                qc[n][0] = __shfl_sync(0xffffffffu, back, 8 * t4) * p.scale_log2;
-                qc[n][1] = __shfl_sync(0xffffffffu, back, 8 * t4 + 4) * p.scale_log2;
-            } else {
-#pragma unroll
-                for (int s = 0; s < kSteps; ++s)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e)
-                        qb[n][s][e] = r < R ? __ldg(reinterpret_cast<const uint32_t*>(qrow + s * 16 + e * 8 + 2 * t4))
-                                            : 0u;
-                qc[n][0] = qc[n][1] = p.scale_log2;
-            }
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const int rr = row0 + n * 8 + 2 * t4 + h;
                 pos[n][h] = p.causal ? w.len - p.Nq + (rr < R ? rr % p.Nq : 0) : w.len - 1;
+                qc[n][h] = lds32(sQScale + (buf * NT * 8 + n * 8 + 2 * t4 + h) * 4);
             }
-        }
         if (p.causal) pos_min = w.len - p.Nq;
 
         float o[NT][kSteps][4];
@@ -397,15 +485,11 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             l_run[n][0] = l_run[n][1] = 0.f;
         }
 
-        for (int i = 0; i < n_here; ++i, ++t) {
-            ok = ok && mbar_wait(&full[st], phase, abort_flag, kCdSiteFull);
-            ok = __all_sync(0xffffffffu, ok);
-            if (!ok) continue;
-            const uint32_t kb = sK + st * L::kTileBytes, vb = sV + st * L::kTileBytes;
-            const int key0 = (w.tile + i) * kCdKeys + kw;    // slot of the warp's first key
+        // One tile.  kEdge: some key of the warp's 16 is hidden from some row.
+        auto tile = [&](auto edge_c, uint32_t kb, uint32_t vb, int key0) {
+            constexpr bool kEdge = decltype(edge_c)::value;
             const int kA = key0 + g8, kB = kA + 8;           // this lane's two keys in S^T
-            const bool edge = key0 + 15 > pos_min;           // some key is hidden from some row (warp-uniform)
-            const bool clear = key0 + 15 >= w.len;           // some key is behind the length
+            const bool clear = kEdge && key0 + 15 >= w.len;
             if (clear) {
                 // V rows behind the length may hold NaN, and 0 x NaN is NaN
                 constexpr int kChunks = D * L::kElem / 16;
@@ -422,7 +506,6 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
             for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
             float ksA = 1.f, ksB = 1.f, vsA = 1.f, vsB = 1.f;
-            const int mi = lane >> 3;
             if constexpr (kHalf) {
                 const uint32_t sc = sS + st * 2 * L::kScaleBytes + (kw + g8) * 4;
                 ksA = lds32(sc);
@@ -431,9 +514,8 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                 vsB = lds32(sc + L::kScaleBytes + 32);
 #pragma unroll
                 for (int hh = 0; hh < D / 64; ++hh) {
-                    const int c = D == 128 ? 2 * t4 + hh : t4;
-                    const uint4 ca = lds128(kb + chunk_off<D, kFmt>(kw + g8, c));
-                    const uint4 cb = lds128(kb + chunk_off<D, kFmt>(kw + g8 + 8, c));
+                    const uint32_t at = chunk_at(kb + k_at, hh);
+                    const uint4 ca = lds128(at), cb = lds128(at + 8 * D);
                     const uint32_t wa[4] = {ca.x, ca.y, ca.z, ca.w}, wb[4] = {cb.x, cb.y, cb.z, cb.w};
 #pragma unroll
                     for (int w4 = 0; w4 < 4; ++w4) {
@@ -441,18 +523,22 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                         unpack4<kFmt>(wa[w4], a0, a2);
                         unpack4<kFmt>(wb[w4], a1, a3);
 #pragma unroll
-                        for (int n = 0; n < NT; ++n)
-                            mma16<true>(s[n], a0, a1, a2, a3, qb[n][4 * hh + w4][0], qb[n][4 * hh + w4][1]);
+                        for (int n = 0; n < NT; ++n) {
+                            const uint2 q = lds64(qf + (n * kSteps + 4 * hh + w4) * 256);
+                            mma16<true>(s[n], a0, a1, a2, a3, q.x, q.y);
+                        }
                     }
                 }
             } else {
-                const int krow = kw + (mi & 1) * 8 + (lane & 7);   // matrices: (keys lo, hi) x (d lo, hi)
 #pragma unroll
                 for (int kk = 0; kk < kSteps; ++kk) {
                     uint32_t a[4];
-                    ldsm4(kb + chunk_off<D, kFmt>(krow, 2 * kk + (mi >> 1)), a);
+                    ldsm4(chunk_at(kb + k_at, 2 * kk), a);
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16<false>(s[n], a[0], a[1], a[2], a[3], qb[n][kk][0], qb[n][kk][1]);
+                    for (int n = 0; n < NT; ++n) {
+                        const uint2 q = lds64(qf + (n * kSteps + kk) * 256);
+                        mma16<false>(s[n], a[0], a[1], a[2], a[3], q.x, q.y);
+                    }
                 }
             }
             // ---- mask, online softmax (rows 2 t4, 2 t4 + 1; keys kA, kB).  Element e is
@@ -464,16 +550,19 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     y[n][e] = fmaf(s[n][e], ((e >> 1) ? ksB : ksA) * qc[n][e & 1], nm[n][e & 1]);
-                    if (edge && ((e >> 1) ? kB : kA) > pos[n][e & 1]) y[n][e] = -INFINITY;
+                    if (kEdge && ((e >> 1) ? kB : kA) > pos[n][e & 1]) y[n][e] = -INFINITY;
                     grow |= y[n][e] > kShift + kCdRescale;
                 }
-            if constexpr (kHalf) grow |= (vsA > v_top && kA < w.len) || (vsB > v_top && kB < w.len);
+            if constexpr (kHalf) {
+                grow |= vsA > v_top && (!kEdge || kA < w.len);
+                grow |= vsB > v_top && (!kEdge || kB < w.len);
+            }
             if (__any_sync(0xffffffffu, grow)) {
                 // a maximum grew by more than kCdRescale, or a V scale past the
                 // bound: take the new ones and bring the sums so far to them
                 float vfac = 1.f;
                 if constexpr (kHalf) {
-                    float vm = fmaxf(kA < w.len ? vsA : 0.f, kB < w.len ? vsB : 0.f);
+                    float vm = fmaxf(!kEdge || kA < w.len ? vsA : 0.f, !kEdge || kB < w.len ? vsB : 0.f);
 #pragma unroll
                     for (int k = 4; k <= 16; k <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
                     const float top = fmaxf(v_top, pow2_at_least(vm));
@@ -486,8 +575,8 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     float alpha[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float xa = y[n][h] == -INFINITY ? -INFINITY : s[n][h] * (ksA * qc[n][h]);
-                        const float xb = y[n][2 + h] == -INFINITY ? -INFINITY : s[n][2 + h] * (ksB * qc[n][h]);
+                        const float xa = kEdge && y[n][h] == -INFINITY ? -INFINITY : s[n][h] * (ksA * qc[n][h]);
+                        const float xb = kEdge && y[n][2 + h] == -INFINITY ? -INFINITY : s[n][2 + h] * (ksB * qc[n][h]);
                         float mx = fmaxf(xa, xb);
 #pragma unroll
                         for (int k = 4; k <= 16; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
@@ -497,10 +586,9 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                         nm[n][h] = kShift - m_new;
                         l_run[n][h] *= alpha[h];
                         alpha[h] *= vfac;
-                        y[n][h] = xa + nm[n][h];            // -inf + inf, where no key was seen yet:
-                        y[n][2 + h] = xb + nm[n][h];        // put right below
-                        if (xa == -INFINITY) y[n][h] = -INFINITY;
-                        if (xb == -INFINITY) y[n][2 + h] = -INFINITY;
+                        // -inf + inf is NaN where a row has seen no key yet
+                        y[n][h] = kEdge && xa == -INFINITY ? xa : xa + nm[n][h];
+                        y[n][2 + h] = kEdge && xb == -INFINITY ? xb : xb + nm[n][h];
                     }
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j) {
@@ -526,7 +614,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     for (int e = 0; e < 4; ++e) {
                         pw[e] *= (e >> 1) ? vsB : vsA;
                         // a hidden key's scale may be anything
-                        if (edge && y[n][e] == -INFINITY) pw[e] = 0.f;
+                        if (kEdge && y[n][e] == -INFINITY) pw[e] = 0.f;
                     }
                     pb[n][0] = turn8x8(pack_half2(pw[0], pw[1]));
                     pb[n][1] = turn8x8(pack_half2(pw[2], pw[3]));
@@ -537,33 +625,41 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             }
             // ---- O^T (D x rows) += V^T P^T
             if constexpr (kHalf) {
-                // matrices: (keys lo, hi) x (chunk of 16 values j, j + 1)
-                const int vrow = kw + (mi & 1) * 8 + (lane & 7);
 #pragma unroll
                 for (int j = 0; j < kSteps; j += 2) {
                     uint32_t r[4];
-                    ldsm4_t(vb + chunk_off<D, kFmt>(vrow, j + (mi >> 1)), r);
+                    ldsm4_t(chunk_at(vb + v_at, j), r);
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        uint32_t a0, a1, a2, a3;   // rows d = 16 j + 2 g8 (a0, a2) and + 1 (a1, a3)
-                        unpack4<kFmt>(__byte_perm(r[2 * u], 0u, 0x3120), a0, a1);
-                        unpack4<kFmt>(__byte_perm(r[2 * u + 1], 0u, 0x3120), a2, a3);
+                        uint32_t a0, a1, a2, a3;   // rows d = 16 (j + u) + 2 g8 (a0, a2) and + 1 (a1, a3)
+                        unpack4_pairs<kFmt>(r[2 * u], a0, a1);
+                        unpack4_pairs<kFmt>(r[2 * u + 1], a2, a3);
 #pragma unroll
                         for (int n = 0; n < NT; ++n) mma16<true>(o[n][j + u], a0, a1, a2, a3, pb[n][0], pb[n][1]);
                     }
                 }
             } else {
-                // matrices: (d lo, hi) x (keys lo, hi)
-                const int vrow = kw + (mi >> 1) * 8 + (lane & 7);
 #pragma unroll
                 for (int j = 0; j < kSteps; ++j) {
                     uint32_t r[4];
-                    ldsm4_t(vb + chunk_off<D, kFmt>(vrow, 2 * j + (mi & 1)), r);
+                    ldsm4_t(chunk_at(vb + v_at, 2 * j), r);
 #pragma unroll
                     for (int n = 0; n < NT; ++n) mma16<false>(o[n][j], r[0], r[1], r[2], r[3], pb[n][0], pb[n][1]);
                 }
             }
             if (clear) fence_proxy_async_smem();   // the zeros before the next copy into this stage
+        };
+
+        for (int i = w.t0; i < w.t1; ++i) {
+            ok = ok && mbar_wait(&full[st], phase, abort_flag, kCdSiteFull);
+            ok = __all_sync(0xffffffffu, ok);
+            if (!ok) continue;
+            const uint32_t kb = sK + st * L::kTileBytes, vb = sV + st * L::kTileBytes;
+            const int key0 = i * kCdKeys + kw;               // slot of the warp's first key
+            if (__any_sync(0xffffffffu, key0 + 15 > pos_min))
+                tile(std::true_type{}, kb, vb, key0);
+            else
+                tile(std::false_type{}, kb, vb, key0);
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
             if (++st == kStages) {
@@ -571,6 +667,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                 phase ^= 1u;
             }
         }
+        if (lane == 0) mbar_arrive(&q_empty[buf]);
 
         // ---- the four warps' parts of the unit, joined in shared memory
 #pragma unroll
@@ -589,22 +686,25 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                 }
             if (t4 == 0) ml[warp * 40 + 32] = v_top;
         }
-        const long long unit_end = unit_at + w.tiles;
-        const bool whole = n_here == w.tiles;
-        // a part at the start of the run goes to slot 2 c, one that begins in it to 2 c + 1
-        const bool at_start = unit_at + w.tile == run.x0;
-        const int slot = 2 * static_cast<int>(blockIdx.x) + (at_start ? 0 : 1);
-        if (w.tile == 0 && threadIdx.x == 0) {
-            const int unit = w.b * p.HR + w.hr;
-            const int last = static_cast<int>((unit_end * run.n - 1) / run.total);   // CTA of the last tile
-            p.meta[unit] = make_int2(whole ? -1 : slot, last);
+        // a part that begins before this CTA goes to its slot 2 c, one that ends after it to 2 c + 1
+        const bool whole = w.t0 == 0 && w.t1 == w.tiles;
+        const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
+        if (w.t0 == 0 && threadIdx.x == 0) {
+            const long long end = w.at + p.unit_cost + w.tiles;                      // past the last tile
+            const int last = static_cast<int>((end * w.n - 1) / w.total);            // its CTA
+            p.meta[w.b * p.HR + w.hr] = make_int2(whole ? -1 : slot, last);
         }
         constexpr int kPitch = L::kCols + 4;
+        // 16 threads a row, kCols / 16 columns each
+        constexpr int kPer = L::kCols / 16;
+        const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * kPer;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
+            float M = -INFINITY, wgt[4], Lsum = 0.f, inv = 0.f;
+            const int row = row0 + n * 8 + r;
 #pragma unroll
             for (int dh = 0; dh < D / L::kCols; ++dh) {
-                asm volatile("bar.sync 1, 128;" ::: "memory");   // the previous block has been read
+                if (n + dh > 0) asm volatile("bar.sync 1, 128;" ::: "memory");   // the previous block has been read
 #pragma unroll
                 for (int jj = 0; jj < L::kCols / 16; ++jj) {
                     const int j = dh * (L::kCols / 16) + jj;
@@ -620,193 +720,234 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     }
                 }
                 asm volatile("bar.sync 1, 128;" ::: "memory");
-                // thread -> (row, 4 columns)
-                const int r = threadIdx.x >> 4, c4 = (threadIdx.x & 15) * 4;
-                const int row = row0 + n * 8 + r;
-                float M = -INFINITY, wgt[4], Lsum = 0.f, top = 0.f;
+                if (dh == 0) {
+                    float top = 0.f;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    M = fmaxf(M, ml[q * 40 + n * 8 + r]);
-                    if (kHalf) top = fmaxf(top, ml[q * 40 + 32]);
-                }
+                    for (int q = 0; q < 4; ++q) {
+                        M = fmaxf(M, ml[q * 40 + n * 8 + r]);
+                        if (kHalf) top = fmaxf(top, ml[q * 40 + 32]);
+                    }
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float mq = ml[q * 40 + n * 8 + r];
-                    wgt[q] = mq == -INFINITY ? 0.f : ex2(mq - M);
-                    Lsum += wgt[q] * ml[q * 40 + 16 + n * 8 + r];
-                    if (kHalf) wgt[q] *= ml[q * 40 + 32] * pow2_inverse(top);
+                    for (int q = 0; q < 4; ++q) {
+                        const float mq = ml[q * 40 + n * 8 + r];
+                        wgt[q] = mq == -INFINITY ? 0.f : ex2(mq - M);
+                        Lsum += wgt[q] * ml[q * 40 + 16 + n * 8 + r];
+                        if (kHalf) wgt[q] *= ml[q * 40 + 32] * pow2_inverse(top);
+                    }
+                    // rows without a key: 0; a NaN sum stays NaN
+                    inv = Lsum == 0.f ? 0.f : (kHalf ? top : 1.f) / Lsum;
                 }
-                // rows without a key: 0; a NaN sum stays NaN
-                const float inv = Lsum == 0.f ? 0.f : (kHalf ? top : 1.f) / Lsum;
-                float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+                float acc[kPer];
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    const float4 v = *reinterpret_cast<const float4*>(merge + (q * 8 + r) * kPitch + c4);
-                    acc.x += wgt[q] * v.x;
-                    acc.y += wgt[q] * v.y;
-                    acc.z += wgt[q] * v.z;
-                    acc.w += wgt[q] * v.w;
-                }
-                acc = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-                const float lse = Lsum == 0.f ? -INFINITY : (M + log2f(Lsum) - kShift) * kLn2;
-                const int d = dh * L::kCols + c4;
+                for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < kPer; e += 2) {
+                        const float2 v = *reinterpret_cast<const float2*>(merge + (q * 8 + r) * kPitch + c0 + e);
+                        acc[e] += wgt[q] * v.x;
+                        acc[e + 1] += wgt[q] * v.y;
+                    }
+                const int d = dh * L::kCols + c0;
+                const float lse = d != 0 ? 0.f : (Lsum == 0.f ? -INFINITY : (M + log2f(Lsum) - kShift) * kLn2);
                 if (row < R && ok) {
                     if (whole && p.o_unit == nullptr) {
                         __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.o) + (rows_at + row) * D + d;
-                        *reinterpret_cast<uint2*>(out) = make_uint2(pack_bf16x2(acc.x, acc.y), pack_bf16x2(acc.z, acc.w));
+#pragma unroll
+                        for (int e = 0; e < kPer; e += 2)
+                            *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
                         if (d == 0) p.lse[rows_at + row] = lse;
-                    } else if (whole) {
-                        *reinterpret_cast<float4*>(p.o_unit + (rows_at + row) * D + d) = acc;
-                        if (d == 0) p.lse_unit[rows_at + row] = lse;
                     } else {
-                        const size_t prow = static_cast<size_t>(slot) * (8 * NT) + n * 8 + r;
-                        *reinterpret_cast<float4*>(p.o_part + prow * D + d) = acc;
-                        if (d == 0) p.lse_part[prow] = lse;
+                        const size_t prow = whole ? rows_at + row : static_cast<size_t>(slot) * (8 * NT) + n * 8 + r;
+                        float* out = (whole ? p.o_unit : p.o_part) + prow * D + d;
+#pragma unroll
+                        for (int e = 0; e < kPer; e += 2)
+                            *reinterpret_cast<float2*>(out + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
+                        if (d == 0) (whole ? p.lse_unit : p.lse_part)[prow] = lse;
                     }
                 }
             }
         }
-        w.tile += n_here;
-        if (w.tile == w.tiles) {
-            unit_at = unit_end;
-            w.next_unit(p);
-        }
+        ++unit;
         asm volatile("bar.sync 1, 128;" ::: "memory");   // ml is free again
     }
+    grid_wait();
 }
 
 // Joins the parts of a query row: those of the CTAs that share its unit, and
-// the prefix's.  One CTA a row, a warp for every fourth part.
+// the prefix's.
 //   LSE = log sum_s exp(LSE_s),   O = sum_s exp(LSE_s - LSE) O_s
-template <int D>
+// kWarps warps a row, every kWarps-th part each: a lane finds one part and its
+// weight, so that the loads of the parts' rows that follow depend on nothing.
+template <int D, int kWarps>
 __global__ void __launch_bounds__(128)
-fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f) {
+fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_rows) {
     constexpr int kPer = D / 32;
     __shared__ float sh_m[4], sh_z[4];
     __shared__ float sh_o[4][D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int sub = warp % kWarps;
     const int R = p.G * p.Nq;
-    const int gr = static_cast<int>(blockIdx.x);      // row of [B, Hq, Nq]
+    const int gr = static_cast<int>(blockIdx.x) * (4 / kWarps) + warp / kWarps;   // row of [B, Hq, Nq]
+    if (gr >= n_rows) return;                         // kWarps == 4: the grid is exact
     const int bkv = gr / R, r = gr - bkv * R;
     const int b = bkv / p.Hkv, hkv = bkv - b * p.Hkv;
     const int rb = r / p.rows_cta, in = r - rb * p.rows_cta;
+    grid_wait();                                      // the main kernel's results, and the prefix's
     const int2 meta = p.meta[b * p.HR + hkv * p.RB + rb];
     const bool whole = meta.x < 0;
     if (whole && f.n_cta == 0) return;                // written by the main kernel
     const int own = whole ? 1 : meta.y - (meta.x >> 1) + 1;
     // the prefix unit that holds the row, and the CTAs that share it
-    int pfirst = 0, np = 0, psub = 0, pin = 0, pu = 0;
+    int np = 0, pin = 0;
+    size_t pslot = 0;
     if (f.n_cta > 0) {
         const int prow = b * R + r;
-        pu = hkv * f.n_rowtiles + prow / f.rows_unit;
+        const int pu = hkv * f.n_rowtiles + prow / f.rows_unit;
         pin = prow % f.rows_unit;
-        psub = f.subs;
         const long long total = static_cast<long long>(f.Hkv) * f.n_rowtiles * f.n_tiles;
         const long long ts = static_cast<long long>(pu) * f.n_tiles;
-        pfirst = static_cast<int>(((ts + 1) * f.n_cta - 1) / total);
-        np = (static_cast<int>(((ts + f.n_tiles) * f.n_cta - 1) / total) - pfirst + 1) * psub;
+        const int first = static_cast<int>(((ts + 1) * f.n_cta - 1) / total);
+        np = (static_cast<int>(((ts + f.n_tiles) * f.n_cta - 1) / total) - first + 1) * f.subs;
+        pslot = static_cast<size_t>(first + pu) * f.subs;
     }
     const int n = own + np;
-    auto part = [&](int i, const float*& o, float& lse) {
-        if (i < own) {
-            if (whole) {
-                o = p.o_unit + static_cast<size_t>(gr) * D;
-                lse = p.lse_unit[gr];
-            } else {
-                const int slot = i == 0 ? meta.x : 2 * ((meta.x >> 1) + i);
-                const size_t prow = static_cast<size_t>(slot) * p.rows_cta + in;
-                o = p.o_part + prow * D;
-                lse = p.lse_part[prow];
-            }
-        } else {
-            const int k = i - own;
-            const size_t prow = (static_cast<size_t>(pfirst + k / psub + pu) * psub + k % psub) * f.rows_unit + pin;
-            o = f.o_part + prow * D;
-            lse = f.lse_part[prow];
-        }
-    };
     float M = -INFINITY, Z = 0.f, acc[kPer];
 #pragma unroll
     for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
-    for (int s = warp; s < n; s += 4) {
-        const float* o;
-        float lse;
-        part(s, o, lse);
-        if (lse == -INFINITY) continue;               // no key in this part; its o may be unwritten
-        const float m_new = fmaxf(M, lse);
-        const float a = __expf(M - m_new), e = expf(lse - m_new);
+    for (int s0 = sub; s0 < n; s0 += 32 * kWarps) {
+        const int s = s0 + lane * kWarps;
+        const float* o = nullptr;
+        float lse = -INFINITY;
+        if (s < n) {
+            size_t prow;
+            if (s >= own) {
+                prow = (pslot + static_cast<size_t>(s - own)) * f.rows_unit + pin;
+                o = f.o_part + prow * D;
+                lse = f.lse_part[prow];
+            } else if (whole) {
+                o = p.o_unit + static_cast<size_t>(gr) * D;
+                lse = p.lse_unit[gr];
+            } else {
+                prow = static_cast<size_t>(s == 0 ? meta.x : 2 * ((meta.x >> 1) + s)) * p.rows_cta + in;
+                o = p.o_part + prow * D;
+                lse = p.lse_part[prow];
+            }
+        }
+        float top = lse;                              // NaN leaves the maximum alone and its weight NaN
+#pragma unroll
+        for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+        const float m_new = fmaxf(M, top);
+        const float a = m_new == -INFINITY ? 1.f : expf(M - m_new);
+        const float e = lse == -INFINITY ? 0.f : expf(lse - m_new);
         M = m_new;
-        Z = Z * a + e;
+        Z = Z * a;
 #pragma unroll
-        for (int i = 0; i < kPer; ++i) acc[i] = acc[i] * a + e * o[lane * kPer + i];
+        for (int i = 0; i < kPer; ++i) acc[i] *= a;
+        const int here = min(32, (n - s0 + kWarps - 1) / kWarps);
+#pragma unroll 8
+        for (int j = 0; j < here; ++j) {
+            const float w = __shfl_sync(0xffffffffu, e, j);
+            const float* oj = reinterpret_cast<const float*>(
+                __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), j));
+            Z += w;
+            float v[kPer];
+            if constexpr (kPer == 4) {
+                const float4 x = __ldcg(reinterpret_cast<const float4*>(oj) + lane);
+                v[0] = x.x;
+                v[1] = x.y;
+                v[2] = x.z;
+                v[3] = x.w;
+            } else {
+                const float2 x = __ldcg(reinterpret_cast<const float2*>(oj) + lane);
+                v[0] = x.x;
+                v[1] = x.y;
+            }
+            // a part without a key may not have written its o
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] = w == 0.f ? acc[i] : fmaf(w, v[i], acc[i]);
+        }
     }
-    if (lane == 0) {
-        sh_m[warp] = M;
-        sh_z[warp] = Z;
+    if constexpr (kWarps > 1) {
+        if (lane == 0) {
+            sh_m[warp] = M;
+            sh_z[warp] = Z;
+        }
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) sh_o[warp][lane * kPer + i] = acc[i];
+        __syncthreads();
+        if (sub != 0) return;
+        M = -INFINITY;
+        Z = 0.f;
+#pragma unroll
+        for (int i = 0; i < kPer; ++i) acc[i] = 0.f;
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) M = fmaxf(M, sh_m[q]);
+#pragma unroll
+        for (int q = 0; q < kWarps; ++q) {
+            const float e = sh_z[q] == 0.f ? 0.f : expf(sh_m[q] - M);
+            Z += e * sh_z[q];
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) acc[i] += e * sh_o[q][lane * kPer + i];
+        }
     }
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) sh_o[warp][lane * kPer + i] = acc[i];
-    __syncthreads();
-    if (warp != 0) return;
-    float Mt = -INFINITY, Zt = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) Mt = fmaxf(Mt, sh_m[q]);
-    float out[kPer];
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) out[i] = 0.f;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-        const float e = sh_m[q] == -INFINITY && sh_z[q] == 0.f ? 0.f : expf(sh_m[q] - Mt);
-        Zt += e * sh_z[q];
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) out[i] += e * sh_o[q][lane * kPer + i];
-    }
-    const float inv = Zt == 0.f ? 0.f : 1.f / Zt;
+    const float inv = Z == 0.f ? 0.f : 1.f / Z;
     __nv_bfloat16* dst = reinterpret_cast<__nv_bfloat16*>(p.o) + static_cast<size_t>(gr) * D + lane * kPer;
 #pragma unroll
-    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(out[i] * inv, out[i + 1] * inv);
-    if (lane == 0) p.lse[gr] = Zt == 0.f ? -INFINITY : Mt + logf(Zt);
+    for (int i = 0; i < kPer; i += 2) *reinterpret_cast<uint32_t*>(dst + i) = pack_bf16x2(acc[i] * inv, acc[i + 1] * inv);
+    if (lane == 0) p.lse[gr] = Z == 0.f ? -INFINITY : M + logf(Z);
 }
 
 template <int D, int kFmt, int NT>
-cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p, cudaStream_t stream) {
+cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p, bool after_prefix,
+               cudaStream_t stream) {
     auto kern = fa_cache_decode_kernel<D, kFmt, NT>;
     static SmemOptIn opt_in;
-    const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(kern), CdLayout<D, kFmt>::kAlloc);
+    const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(kern), CdLayout<D, kFmt, NT>::kAlloc);
     if (e != cudaSuccess) return e;
-    kern<<<p.n_cta, kCdThreads, CdLayout<D, kFmt>::kAlloc, stream>>>(tk, tv, p);
+    constexpr int kSmem = CdLayout<D, kFmt, NT>::kAlloc;
+    if (after_prefix) return launch_dependent(kern, p.n_cta, kCdThreads, kSmem, stream, tk, tv, p);
+    kern<<<p.n_cta, kCdThreads, kSmem, stream>>>(tk, tv, p);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t go_fmt(int fmt, const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p,
-                   cudaStream_t stream) {
+                   bool after_prefix, cudaStream_t stream) {
     const bool one = p.rows_cta == 8;
-    if (fmt == 0) return one ? go<D, 0, 1>(tk, tv, p, stream) : go<D, 0, 2>(tk, tv, p, stream);
-    if (fmt == 1) return one ? go<D, 1, 1>(tk, tv, p, stream) : go<D, 1, 2>(tk, tv, p, stream);
-    return one ? go<D, 2, 1>(tk, tv, p, stream) : go<D, 2, 2>(tk, tv, p, stream);
+    if (fmt == 0) return one ? go<D, 0, 1>(tk, tv, p, after_prefix, stream) : go<D, 0, 2>(tk, tv, p, after_prefix, stream);
+    if (fmt == 1) return one ? go<D, 1, 1>(tk, tv, p, after_prefix, stream) : go<D, 1, 2>(tk, tv, p, after_prefix, stream);
+    return one ? go<D, 2, 1>(tk, tv, p, after_prefix, stream) : go<D, 2, 2>(tk, tv, p, after_prefix, stream);
 }
 
 }  // namespace
 
-int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta) {
-    const int nt = rows_cta / 8;
-    if (D == 128) return fmt == 0 ? CdLayout<128, 0>::kCtas(nt) : CdLayout<128, 1>::kCtas(nt);
-    return fmt == 0 ? CdLayout<64, 0>::kCtas(nt) : CdLayout<64, 1>::kCtas(nt);
+int cache_decode_ctas_per_sm(int D, int fmt) {
+    if (D == 128) return fmt == 0 ? CdLayout<128, 0, 1>::kCtas : CdLayout<128, 1, 1>::kCtas;
+    return fmt == 0 ? CdLayout<64, 0, 1>::kCtas : CdLayout<64, 1, 1>::kCtas;
 }
 
+// Measured with 64 sequences of up to 1000 slots (8 rows): 32 us at 0, 25 at 1,
+// 23 at 2; with 48 of up to 8100 (12 rows): 60 at 0, 53 at 2, 51 at 4.
+int cache_decode_unit_cost(int rows_cta) { return rows_cta == 8 ? 2 : 4; }
+
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const CacheDecodeParams& p, cudaStream_t stream) {
-    return D == 128 ? go_fmt<128>(fmt, tk, tv, p, stream) : go_fmt<64>(fmt, tk, tv, p, stream);
+                                const CacheDecodeParams& p, bool after_prefix, cudaStream_t stream) {
+    return D == 128 ? go_fmt<128>(fmt, tk, tv, p, after_prefix, stream)
+                    : go_fmt<64>(fmt, tk, tv, p, after_prefix, stream);
 }
 
 cudaError_t launch_cache_combine(int D, const CacheDecodeParams& p, const PrefixParams& f, cudaStream_t stream) {
-    const unsigned rows = static_cast<unsigned>(p.B) * p.Hkv * p.G * p.Nq;
+    const int rows = p.B * p.Hkv * p.G * p.Nq;
+    // One warp a row once that fills the SMs; below, four share a row's parts,
+    // of which there are the more the fewer rows there are.
+    const bool many = rows >= 1024;
+    const unsigned grid = many ? static_cast<unsigned>((rows + 3) / 4) : static_cast<unsigned>(rows);
     if (D == 128)
-        fa_cache_combine_kernel<128><<<rows, 128, 0, stream>>>(p, f);
-    else
-        fa_cache_combine_kernel<64><<<rows, 128, 0, stream>>>(p, f);
-    return cudaGetLastError();
+        return many ? launch_dependent(fa_cache_combine_kernel<128, 1>, grid, 128u, 0, stream, p, f, rows)
+                    : launch_dependent(fa_cache_combine_kernel<128, 4>, grid, 128u, 0, stream, p, f, rows);
+    return many ? launch_dependent(fa_cache_combine_kernel<64, 1>, grid, 128u, 0, stream, p, f, rows)
+                : launch_dependent(fa_cache_combine_kernel<64, 4>, grid, 128u, 0, stream, p, f, rows);
 }
 
 }  // namespace fa

@@ -177,6 +177,25 @@ struct SmemOptIn {
     }
 };
 
+// Launch of a kernel that may start before the kernel ahead of it in the stream
+// has ended; it waits for it itself (grid_wait) where it needs its results, and
+// in any case before it ends.
+template <class... Params, class... Args>
+cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
+                             const Args&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid);
+    cfg.blockDim = dim3(block);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // bf16 rows of D contiguous values, indexed [b, h, n] by strides in elements.
 struct RopeRows {
     __nv_bfloat16* data;
@@ -237,12 +256,15 @@ struct CacheDecodeParams {
     int B, Hkv, G, Nq, capacity, causal;
     int rows_cta, RB, HR;    // query rows a CTA holds (8 or 16), row blocks of a K/V head, Hkv * RB
     int n_cta;
+    int unit_cost;           // positions a unit counts besides its tiles
     float scale_log2;
 };
 // CTAs of the cache part that fit on an SM at once (shared memory and registers).
-int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta);
+int cache_decode_ctas_per_sm(int D, int fmt);
+int cache_decode_unit_cost(int rows_cta);
+// after_prefix: the prefix kernel is the one ahead of it in the stream.
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const CacheDecodeParams& p, cudaStream_t stream);
+                                const CacheDecodeParams& p, bool after_prefix, cudaStream_t stream);
 
 // Shared prefix (fa_prefix.cu).  A unit is rows_unit of the B * G * Nq rows of
 // a K/V head; the part of unit u that CTA c computes lies in slot c + u of

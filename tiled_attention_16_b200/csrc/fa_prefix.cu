@@ -75,12 +75,11 @@ struct Part {
     int u, t0, n;
 };
 
-__device__ __forceinline__ bool next_part(const PrefixParams& p, long long& x, long long x1, Part& w) {
+__device__ __forceinline__ bool next_part(const PrefixParams& p, int& x, int x1, Part& w) {
     if (x >= x1) return false;
-    w.u = static_cast<int>(x / p.n_tiles);
-    w.t0 = static_cast<int>(x - static_cast<long long>(w.u) * p.n_tiles);
-    const long long left = x1 - x;
-    w.n = static_cast<int>(left < p.n_tiles - w.t0 ? left : p.n_tiles - w.t0);
+    w.u = x / p.n_tiles;
+    w.t0 = x - w.u * p.n_tiles;
+    w.n = min(x1 - x, p.n_tiles - w.t0);
     x += w.n;
     return true;
 }
@@ -129,10 +128,11 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_slot;
+    grid_launch_dependents();   // the cache part needs nothing from here and may take SMs as they come free
 
-    const long long total = static_cast<long long>(p.Hkv) * p.n_rowtiles * p.n_tiles;
-    const long long x0 = total * blockIdx.x / gridDim.x;
-    const long long x1 = total * (blockIdx.x + 1) / gridDim.x;
+    const int total = p.Hkv * p.n_rowtiles * p.n_tiles;
+    const int x0 = static_cast<int>(static_cast<long long>(total) * blockIdx.x / gridDim.x);
+    const int x1 = static_cast<int>(static_cast<long long>(total) * (blockIdx.x + 1) / gridDim.x);
 
     if (warp == 9) {
         // ------------------------------------------------------------ producer
@@ -142,7 +142,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             int gk = 0, issued = 0;
             bool ok = true;
             Part w;
-            for (long long x = x0; ok && next_part(p, x, x1, w);) {
+            for (int x = x0; ok && next_part(p, x, x1, w);) {
                 const int hkv = w.u / p.n_rowtiles;
                 for (int j = 0; j < w.n; ++j, ++gk) {
                     const int st = gk % kStages;
@@ -194,7 +194,7 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                 tc_commit(&s_full[s]);
                 return true;
             };
-            for (long long x = x0; ok && next_part(p, x, x1, w);) {
+            for (int x = x0; ok && next_part(p, x, x1, w);) {
                 const int n_steps = w.n * kTileSteps;
                 if (!(ok = mbar_wait(q_full, parts & 1, abort_flag, kPfQ))) break;
                 tc_fence_after();
@@ -230,30 +230,37 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         const float c = p.scale_log2;
         const int R = p.G * p.Nq;                      // rows of one sequence
         const int n_rows = p.B * R;                    // rows of one K/V head
-        // Q row of this thread (kRows2), or half of row r (both warpgroups load the one tile)
+        // Q rows to shared memory, D / 8 lanes a row: a warp loads the 32 rows of its
+        // lane quarter of its own tile (kRows2), or 16 of them (both warpgroups load
+        // the one tile)
         auto load_q = [&](int u) {
             const int hkv = u / p.n_rowtiles;
-            const int row = (u - hkv * p.n_rowtiles) * p.rows_unit + (kRows2 ? s * kTileM : 0) + r;
-            constexpr int kChunks = kRows2 ? D / 8 : D / 16;
-            const int c0 = kRows2 ? 0 : s * kChunks;
-            const bool real = row < n_rows;
-            const int b = real ? row / R : 0;
-            const uint4* src = reinterpret_cast<const uint4*>(
-                reinterpret_cast<const __nv_bfloat16*>(p.q) +
-                (static_cast<size_t>(b * p.Hkv + hkv) * R + (real ? row - b * R : 0)) * D);
+            constexpr int kLanes = D / 8, kStep = 32 / kLanes;
+            const int rw = (kRows2 ? (warp & 3) * 32 : warp * 16) + lane / kLanes, ch = lane % kLanes;
+            const int first = (u - hkv * p.n_rowtiles) * p.rows_unit + (kRows2 ? s * kTileM : 0) + rw;
             uint8_t* dst = smem + L::kQ + (kRows2 ? s * L::kTileBytes : 0);
+            constexpr int kLoads = (kRows2 ? 32 : 16) / kStep;
+            uint4 v[kLoads];   // all in flight at once
+            int b = first / R, in = first - b * R;
 #pragma unroll
-            for (int k = 0; k < kChunks; ++k) {
-                const uint4 v = real ? __ldg(src + c0 + k) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(dst + sw128_offset(r, (c0 + k) * 8, kTileM)) = v;
+            for (int k = 0; k < kLoads; ++k) {
+                v[k] = make_uint4(0u, 0u, 0u, 0u);
+                if (first + k * kStep < n_rows)
+                    v[k] = __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const __nv_bfloat16*>(p.q) +
+                                                                (static_cast<size_t>(b * p.Hkv + hkv) * R + in) * D) +
+                                 ch);
+                for (in += kStep; in >= R; in -= R) ++b;
             }
+#pragma unroll
+            for (int k = 0; k < kLoads; ++k)
+                *reinterpret_cast<uint4*>(dst + sw128_offset(rw + k * kStep, ch * 8, kTileM)) = v[k];
             fence_proxy_async_smem();
             mbar_arrive(q_full);
         };
         bool ok = true;
         int cs = 0;       // score blocks of this warpgroup so far
         int parts = 0;
-        long long x = x0;
+        int x = x0;
         Part w;
         bool more = next_part(p, x, x1, w);
         if (more) load_q(w.u);
@@ -342,19 +349,31 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             const size_t prow = static_cast<size_t>(blockIdx.x + done.u) * 256 + s * kTileM + r;
             const bool valid = row < n_rows;
             if (n_here > 0) {
+                // 8 columns of 8 rows a store, whole 32-byte sectors
                 const float inv_l = 1.f / l;
+                const int row_w = row - lane;                          // the warp's first row
+                float* out = p.o_part + (prow - lane) * D;
 #pragma unroll 1
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t ov[32];
-                    tmem_ld32(tO + q * 32, ov);
-                    tmem_ld_wait();
-                    if (valid) {
-                        float4* dst = reinterpret_cast<float4*>(p.o_part + prow * D + q * 32);
+                for (int half = 0; half < 2; ++half) {
+                    const int ra = half * 16 + (lane >> 2), rb = ra + 8;
+                    const float ia = __shfl_sync(0xffffffffu, inv_l, ra), ib = __shfl_sync(0xffffffffu, inv_l, rb);
+                    const bool va = row_w + ra < n_rows, vb = row_w + rb < n_rows;
+#pragma unroll 1
+                    for (int q = 0; q < D / 32; ++q) {
+                        uint32_t ov[16];
+                        tmem_ld_16x32(tO + (static_cast<uint32_t>(half * 16) << 16) + q * 32, ov);
+                        tmem_ld_wait();
 #pragma unroll
-                        for (int t = 0; t < 8; ++t)
-                            dst[t] = make_float4(__uint_as_float(ov[4 * t]) * inv_l, __uint_as_float(ov[4 * t + 1]) * inv_l,
-                                                 __uint_as_float(ov[4 * t + 2]) * inv_l,
-                                                 __uint_as_float(ov[4 * t + 3]) * inv_l);
+                        for (int c8 = 0; c8 < 4; ++c8) {
+                            const int d = q * 32 + c8 * 8 + (lane & 3) * 2;
+                            if (va)
+                                *reinterpret_cast<float2*>(out + static_cast<size_t>(ra) * D + d) =
+                                    make_float2(__uint_as_float(ov[4 * c8]) * ia, __uint_as_float(ov[4 * c8 + 1]) * ia);
+                            if (vb)
+                                *reinterpret_cast<float2*>(out + static_cast<size_t>(rb) * D + d) =
+                                    make_float2(__uint_as_float(ov[4 * c8 + 2]) * ib,
+                                                __uint_as_float(ov[4 * c8 + 3]) * ib);
+                        }
                     }
                 }
                 if (valid) p.lse_part[prow] = (m_used + pf_lg2(l)) * 0.69314718055994531f;
