@@ -104,28 +104,33 @@ fa_cache_write_kernel(const CacheWriteParams p) {
     const unsigned per = n_tiles * h_tiles;
     const unsigned b = blockIdx.x / per, in = blockIdx.x - b * per;
     if (b >= static_cast<unsigned>(p.B)) return;            // the other tensor has more tiles
-    const unsigned n0 = in / h_tiles * (kSlots * kRows >> shift), h0 = (in % h_tiles) << shift;
+    // this thread's first row, and what the tokens of its others are apart
+    const int r = static_cast<int>(threadIdx.x / kLanes);
+    const int n = static_cast<int>(in / h_tiles * (kSlots * kRows >> shift)) + (r >> shift);
+    const int h = static_cast<int>((in % h_tiles) << shift) + (r & ((1 << shift) - 1));
+    const int dn = kSlots >> shift;
+    // tokens n in [lo, hi) have a slot
     const long long start = __ldg(p.start + b);
     const int cnt = p.count ? min(__ldg(p.count + b), p.N) : p.N;
+    const int lo = static_cast<int>(min(max(0ll, -start), static_cast<long long>(p.N)));
+    const int hi = h < p.H ? static_cast<int>(max(min(static_cast<long long>(cnt), p.capacity - start), -1ll)) : -1;
+    const uint4* src = reinterpret_cast<const uint4*>(x.data + b * x.stride_b + h * x.stride_h + n * x.stride_n) + lane;
+    const long long step = dn * x.stride_n / 8;
+    const size_t slot = static_cast<size_t>((static_cast<long long>(b) * p.H + h) * p.capacity + start + n);
     uint4 raw[kRows];
-    long long slot[kRows];   // row of the cache, -1: not written
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const int r = static_cast<int>(threadIdx.x / kLanes) + i * kSlots;
-        const int n = static_cast<int>(n0) + (r >> shift), h = static_cast<int>(h0) + (r & ((1 << shift) - 1));
-        const long long to = start + n;
         raw[i] = make_uint4(0u, 0u, 0u, 0u);
-        slot[i] = -1;
-        if (n < cnt && h < p.H && to >= 0 && to < p.capacity) {
-            slot[i] = (static_cast<long long>(b) * p.H + h) * p.capacity + to;
-            raw[i] = __ldg(reinterpret_cast<const uint4*>(x.data + b * x.stride_b + h * x.stride_h + n * x.stride_n) +
-                           lane);
-        }
+        if (n + i * dn >= lo && n + i * dn < hi) raw[i] = __ldg(src + i * step);
     }
+    uint8_t* dst = cache + slot * (kFmt == 0 ? 2 * D : D) + lane * (kFmt == 0 ? 16 : 8);
+    float* scale_at = kFmt == 0 ? nullptr : scales + slot;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
+        const bool real = n + i * dn >= lo && n + i * dn < hi;
         if constexpr (kFmt == 0) {
-            if (slot[i] >= 0) *(reinterpret_cast<uint4*>(cache + slot[i] * (2 * D)) + lane) = raw[i];
+            if (real) *reinterpret_cast<uint4*>(dst) = raw[i];
+            dst += dn * (2 * D);
         } else {
             const uint32_t amax = row_amax_bits<kLanes>(raw[i]);
             float scale;
@@ -134,14 +139,17 @@ fa_cache_write_kernel(const CacheWriteParams p) {
                 c = make_uint2(0u, 0u);
                 scale = __uint_as_float(0x7fc00000u);
             }
-            if (slot[i] >= 0) {
-                *(reinterpret_cast<uint2*>(cache + slot[i] * D) + lane) = c;
-                if (lane == 0) scales[slot[i]] = scale;
+            if (real) {
+                *reinterpret_cast<uint2*>(dst) = c;
+                if (lane == 0) *scale_at = scale;
             }
+            dst += dn * D;
+            scale_at += dn;
         }
     }
 }
 
+// A CTA reads consecutive slots of one (sequence, head).
 template <int D, int kFmt>
 __global__ void __launch_bounds__(kCacheThreads)
 fa_cache_read_kernel(const CacheReadParams p) {
@@ -151,35 +159,33 @@ fa_cache_read_kernel(const CacheReadParams p) {
     const uint8_t* cache = static_cast<const uint8_t*>(blockIdx.y ? p.v_cache : p.k_cache);
     const float* scales = blockIdx.y ? p.v_scale : p.k_scale;
     __nv_bfloat16* out = static_cast<__nv_bfloat16*>(blockIdx.y ? p.v_out : p.k_out);
-    const long long first = static_cast<long long>(blockIdx.x) * (kSlots * kRows) + threadIdx.x / kLanes;
+    const unsigned tiles = (static_cast<unsigned>(p.N) + kSlots * kRows - 1) / (kSlots * kRows);
+    const unsigned bh = blockIdx.x / tiles;
+    const int n = static_cast<int>((blockIdx.x - bh * tiles) * (kSlots * kRows) + threadIdx.x / kLanes);
+    const int len = p.lens ? min(__ldg(p.lens + bh / static_cast<unsigned>(p.H)), p.capacity) : p.capacity;
+    const size_t slot = static_cast<size_t>(bh) * p.capacity + n;
+    const uint8_t* src = cache + slot * (kFmt == 0 ? 2 * D : D) + lane * (kFmt == 0 ? 16 : 8);
     uint4 raw[kRows];
     float scale[kRows];
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const long long row = first + i * kSlots;
         raw[i] = make_uint4(0u, 0u, 0u, 0u);   // rows behind the length: codes 0, scale 0
         scale[i] = 0.f;
-        if (row < p.rows) {
-            const unsigned bh = static_cast<unsigned>(row) / static_cast<unsigned>(p.N);
-            const int n = static_cast<int>(static_cast<unsigned>(row) - bh * static_cast<unsigned>(p.N));
-            const int len = p.lens ? __ldg(p.lens + bh / static_cast<unsigned>(p.H)) : p.capacity;
-            if (n < len) {
-                const long long slot = static_cast<long long>(bh) * p.capacity + n;
-                if constexpr (kFmt == 0) {
-                    raw[i] = __ldg(reinterpret_cast<const uint4*>(cache + slot * (2 * D)) + lane);
-                } else {
-                    const uint2 c = __ldg(reinterpret_cast<const uint2*>(cache + slot * D) + lane);
-                    raw[i].x = c.x;
-                    raw[i].y = c.y;
-                    scale[i] = __ldg(scales + slot);
-                }
+        if (n + i * kSlots < min(len, p.N)) {
+            if constexpr (kFmt == 0) {
+                raw[i] = __ldg(reinterpret_cast<const uint4*>(src + i * kSlots * 2 * D));
+            } else {
+                const uint2 c = __ldg(reinterpret_cast<const uint2*>(src + i * kSlots * D));
+                raw[i].x = c.x;
+                raw[i].y = c.y;
+                scale[i] = __ldg(scales + slot + i * kSlots);
             }
         }
     }
+    uint4* dst = reinterpret_cast<uint4*>(out + (static_cast<size_t>(bh) * p.N + n) * D) + lane;
 #pragma unroll
     for (int i = 0; i < kRows; ++i) {
-        const long long row = first + i * kSlots;
-        if (row >= p.rows) break;
+        if (n + i * kSlots >= p.N) break;
         uint4 o = raw[i];
         if constexpr (kFmt != 0) {
             const uint32_t c[2] = {raw[i].x, raw[i].y};
@@ -200,7 +206,7 @@ fa_cache_read_kernel(const CacheReadParams p) {
             }
             o = make_uint4(w[0], w[1], w[2], w[3]);
         }
-        *(reinterpret_cast<uint4*>(out + row * D) + lane) = o;
+        dst[i * kSlots * (D / 8)] = o;
     }
 }
 
@@ -212,11 +218,6 @@ cudaError_t cache_dispatch(int D, int fmt, F&& go) {
         return go(d, std::integral_constant<int, 2>{});
     };
     return D == 128 ? with_d(std::integral_constant<int, 128>{}) : with_d(std::integral_constant<int, 64>{});
-}
-
-dim3 cache_grid(int D, long long rows) {
-    const int per = kCacheThreads / (D / 8) * kRows;
-    return dim3(static_cast<unsigned>((rows + per - 1) / per), 2);
 }
 
 }  // namespace
@@ -240,9 +241,10 @@ cudaError_t launch_cache_write(int D, int fmt, CacheWriteParams p, cudaStream_t 
 }
 
 cudaError_t launch_cache_read(int D, int fmt, const CacheReadParams& p, cudaStream_t stream) {
+    const int rows = kCacheThreads / (D / 8) * kRows;
+    const dim3 grid(static_cast<unsigned>(p.BH) * static_cast<unsigned>((p.N + rows - 1) / rows), 2);
     return cache_dispatch(D, fmt, [&](auto d, auto f) {
-        fa_cache_read_kernel<decltype(d)::value, decltype(f)::value>
-            <<<cache_grid(D, p.rows), kCacheThreads, 0, stream>>>(p);
+        fa_cache_read_kernel<decltype(d)::value, decltype(f)::value><<<grid, kCacheThreads, 0, stream>>>(p);
         return cudaGetLastError();
     });
 }

@@ -280,10 +280,10 @@ fa_status fa_cache_read(const fa_cache_shape* shape, int N, const int* lens, con
     p.lens = lens;
     p.k_out = k_out;
     p.v_out = v_out;
+    p.BH = s.B * s.Hkv;
     p.H = s.Hkv;
     p.N = N;
     p.capacity = s.capacity;
-    p.rows = static_cast<long long>(s.B) * s.Hkv * N;
     return status_of(launch_cache_read(s.D, s.format, p, static_cast<cudaStream_t>(stream)));
 }
 

@@ -236,8 +236,7 @@ struct CacheReadParams {
     const float *k_scale, *v_scale;
     const int* lens;
     void *k_out, *v_out;
-    int H, N, capacity;
-    long long rows;          // B * H * N
+    int BH, H, N, capacity;
 };
 cudaError_t launch_cache_write(int D, int fmt, CacheWriteParams p, cudaStream_t stream);
 cudaError_t launch_cache_read(int D, int fmt, const CacheReadParams& p, cudaStream_t stream);
