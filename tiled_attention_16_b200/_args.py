@@ -29,4 +29,4 @@ def want(t, name: str, shape: tuple, dtype, first: torch.Tensor) -> None:
 
 def on_device(index: int):
     """None when `index` is the current CUDA device, else a guard that makes it so."""
-    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
+    return None if torch._C._cuda_getDevice() == index else torch.cuda.device(index)

@@ -147,11 +147,11 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, n: int | None = Non
         with guard:
             return cache_read(k_cache, v_cache, n, lens, k_scale, v_scale, out_k, out_v)
     if out_k is None:
-        out_k = k_cache.new_empty(shape, dtype=torch.bfloat16)
+        out_k = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
     else:
         want(out_k, "out_k", shape, torch.bfloat16, k_cache)
     if out_v is None:
-        out_v = k_cache.new_empty(shape, dtype=torch.bfloat16)
+        out_v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
     else:
         want(out_v, "out_v", shape, torch.bfloat16, k_cache)
     shp = FaCacheShape(B, Hkv, cap, D, fmt)
@@ -219,13 +219,13 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     else:
         want(out, "out", (B, Hq, Nq, D), torch.bfloat16, k_cache)
     if lse is None:
-        lse = q.new_empty((B, Hq, Nq), dtype=torch.float32)
+        lse = torch.empty((B, Hq, Nq), dtype=torch.float32, device=q.device)
     else:
         want(lse, "lse", (B, Hq, Nq), torch.float32, k_cache)
     shp, nbytes = _decode_shape(index, B, Hq, Hkv, Nq, cap, n_prefix, D, fmt,
                                 1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0)
     if workspace is None:
-        workspace = q.new_empty((nbytes,), dtype=torch.uint8)
+        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
         if workspace.get_device() != index:
             raise ValueError(f"all tensors must be on one device: got {q.device} and {workspace.device}")

@@ -114,7 +114,7 @@ def qk_norm_rope(q: torch.Tensor, k: torch.Tensor, q_weight: torch.Tensor, k_wei
     else:
         want(out_q, "out_q", q.shape, torch.bfloat16, q)
     if out_k is None:
-        out_k = q.new_empty(k.shape)
+        out_k = k.new_empty(k.shape)
     else:
         want(out_k, "out_k", k.shape, torch.bfloat16, q)
     index = q.get_device()
@@ -142,11 +142,11 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     shp, qr, kr, qw, kw, freq, pos = _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved)
     want(dq_out, "dq_out", q.shape, torch.bfloat16, q)
     want(dk_out, "dk_out", k.shape, torch.bfloat16, q)
-    B, Hq, N, D = q.shape
+    D, dev = q.shape[3], q.device
     if dq is None:
-        dq = q.new_empty((B, N, Hq, D)).transpose(1, 2)
+        dq = _token_major(q.shape, dev)
     if dk is None:
-        dk = q.new_empty((B, N, k.shape[1], D)).transpose(1, 2)
+        dk = _token_major(k.shape, dev)
     dqr, dkr = check_rows(dq, "dq", q.shape, q), check_rows(dk, "dk", k.shape, q)
     index = q.get_device()
     guard = on_device(index)
@@ -155,9 +155,10 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
             return qk_norm_rope_bwd(dq_out, dk_out, q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved,
                                     dq, dk, workspace)
     L = _rope_lib()
-    dqw, dkw = (q.new_empty((D,), dtype=torch.float32) for _ in range(2))
+    dqw = torch.empty(D, dtype=torch.float32, device=dev)
+    dkw = torch.empty(D, dtype=torch.float32, device=dev)
     if workspace is None:
-        workspace = q.new_empty((_bwd_workspace(D, index),), dtype=torch.uint8)
+        workspace = torch.empty(_bwd_workspace(D, index), dtype=torch.uint8, device=dev)
     elif workspace.get_device() != index:
         raise ValueError(f"all tensors must be on one device: got {q.device} and {workspace.device}")
     st = L.fa_qk_norm_rope_bwd(ctypes.byref(shp), dq_out.data_ptr(), dk_out.data_ptr(), ctypes.byref(qr),
@@ -167,6 +168,12 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     if st != FA_OK:
         raise FAError(st, "fa_qk_norm_rope_bwd")
     return dq, dk, dqw, dkw
+
+
+def _token_major(shape, device) -> torch.Tensor:
+    """A [B, H, N, D] view with the tokens' heads side by side in memory."""
+    B, H, N, D = shape
+    return torch.empty_strided((B, H, N, D), (N * H * D, D, H * D, 1), dtype=torch.bfloat16, device=device)
 
 
 @functools.lru_cache(maxsize=None)
