@@ -130,7 +130,7 @@ fa_status check_decode(const fa_cache_decode_shape* s) {
 // by the lengths it finds.
 struct DecodeCachePlan {
     int rows_cta, RB, n_cta;
-    int rows_unit, subs, n_rowtiles, n_tiles, n_pcta;
+    int rows_unit, n_rowtiles, n_tiles, n_pcta;
     size_t o_part, lse_part, o_unit, lse_unit, meta, po_part, plse_part, total;
 };
 
@@ -139,16 +139,16 @@ DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
     const int R = s.Hq / s.Hkv * s.Nq;
     pl.rows_cta = R <= 8 ? 8 : 16;
     pl.RB = (R + pl.rows_cta - 1) / pl.rows_cta;
-    const long long units = static_cast<long long>(s.B) * s.Hkv * pl.RB;
+    // runs of tiles, and RB CTAs to each
+    const long long units = static_cast<long long>(s.B) * s.Hkv;
     const long long most = units * ((s.capacity + 63LL) / 64);
     const long long resident = static_cast<long long>(sms) * cache_decode_ctas_per_sm(s.D, s.format);
-    pl.n_cta = static_cast<int>(std::min(most, resident));
+    pl.n_cta = static_cast<int>(std::max(1LL, std::min(most, resident / pl.RB))) * pl.RB;
     const long long rows = static_cast<long long>(s.B) * s.Hq * s.Nq;
     if (s.n_prefix > 0) {
         const long long head_rows = static_cast<long long>(s.B) * R;
         const bool two = head_rows > kTileM;     // two row tiles share the key tiles
         pl.rows_unit = two ? 2 * kTileM : kTileM;
-        pl.subs = two ? 1 : 2;
         pl.n_rowtiles = static_cast<int>((head_rows + pl.rows_unit - 1) / pl.rows_unit);
         pl.n_tiles = (s.n_prefix + kTileN - 1) / kTileN;
         const long long units = static_cast<long long>(s.Hkv) * pl.n_rowtiles, tiles = units * pl.n_tiles;
@@ -171,11 +171,11 @@ DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
     const size_t slots = 2 * static_cast<size_t>(pl.n_cta) * pl.rows_cta;
     pl.o_part = take(slots * s.D * 4);
     pl.lse_part = take(slots * 4);
-    pl.meta = take(static_cast<size_t>(units) * 8);
+    pl.meta = take(static_cast<size_t>(units) * pl.RB * 8);
     if (s.n_prefix > 0) {
         pl.o_unit = take(static_cast<size_t>(rows) * s.D * 4);
         pl.lse_unit = take(static_cast<size_t>(rows) * 4);
-        const size_t pslots = (static_cast<size_t>(pl.n_pcta) + static_cast<size_t>(s.Hkv) * pl.n_rowtiles) * 256;
+        const size_t pslots = (static_cast<size_t>(pl.n_pcta) + static_cast<size_t>(s.Hkv) * pl.n_rowtiles) * pl.rows_unit;
         pl.po_part = take(pslots * s.D * 4);
         pl.plse_part = take(pslots * 4);
     }
@@ -336,7 +336,6 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
     p.causal = s.causal ? 1 : 0;
     p.rows_cta = pl.rows_cta;
     p.RB = pl.RB;
-    p.HR = s.Hkv * pl.RB;
     p.n_cta = pl.n_cta;
     p.unit_cost = cache_decode_unit_cost(pl.rows_cta);
     p.scale_log2 = static_cast<float>(static_cast<double>(s.scale) * kLog2e);
@@ -357,7 +356,6 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
         f.Nq = s.Nq;
         f.Np = s.n_prefix;
         f.rows_unit = pl.rows_unit;
-        f.subs = pl.subs;
         f.n_rowtiles = pl.n_rowtiles;
         f.n_tiles = pl.n_tiles;
         f.scale_log2 = p.scale_log2;

@@ -192,14 +192,17 @@ __device__ __forceinline__ int seq_tiles(const CacheDecodeParams& p, int b) {
     return max(1, (seq_len(p, b) + kCdKeys - 1) / kCdKeys);
 }
 
-// Work is dealt out by position: a unit (sequence b; hr = K/V head * row blocks
-// + row block) covers unit_cost positions for what it costs besides its tiles,
-// then one for each tile.  All units lie end to end and CTA c of n takes
-// positions [total c / n, total (c + 1) / n).
+// Work is dealt out by position: a unit (sequence b, K/V head h) covers
+// unit_cost positions for what it costs besides its tiles, then one for each
+// tile.  All units lie end to end and run c of n takes positions
+// [total c / n, total (c + 1) / n).  With more query rows a K/V head than a CTA
+// holds, RB CTAs take a run, one a block of rows, at the same time: the tiles
+// come from HBM once and from L2 for the others (8 sequences of 32K slots, 32
+// rows a head: 174 us with the row blocks as units of their own).
 struct Walk {
-    int x0, x1, total, n;       // the CTA's positions, all positions, CTAs with any
-    int b, hr, at, tiles, len;  // unit, its first position, its tiles, its sequence's length
-    int t0, t1;                 // the CTA's tiles of it
+    int x0, x1, total, n;       // the run's positions, all positions, runs with any
+    int b, h, at, tiles, len;   // unit, its first position, its tiles, its sequence's length
+    int t0, t1;                 // the run's tiles of it
 
     __device__ __forceinline__ void enter(const CacheDecodeParams& p) {
         len = seq_len(p, b);
@@ -209,7 +212,7 @@ struct Walk {
         t0 = max(0, x0 - at - p.unit_cost);
         t1 = min(tiles, x1 - at - p.unit_cost);
     }
-    // to the first unit from here on that the CTA has tiles of; false: none
+    // to the first unit from here on that the run has tiles of; false: none
     __device__ __forceinline__ bool settle(const CacheDecodeParams& p) {
         while (at < x1) {
             clip(p);
@@ -220,31 +223,31 @@ struct Walk {
     }
     __device__ __forceinline__ void step(const CacheDecodeParams& p) {
         at += tiles + p.unit_cost;
-        if (++hr == p.HR) {
-            hr = 0;
+        if (++h == p.Hkv) {
+            h = 0;
             ++b;
             if (b < p.B) enter(p);
         }
     }
 };
 
-// Warp-wide: CTA c of n, at the unit its positions begin in.
+// Warp-wide: run c of n, at the unit its positions begin in.
 __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int n, int lane) {
     Walk w;
     int total = 0;
 #pragma unroll 4
-    for (int b = lane; b < p.B; b += 32) total += (seq_tiles(p, b) + p.unit_cost) * p.HR;
+    for (int b = lane; b < p.B; b += 32) total += (seq_tiles(p, b) + p.unit_cost) * p.Hkv;
     total = __reduce_add_sync(0xffffffffu, total);
-    n = min(n, total);          // every CTA has a position, so those that share a unit are consecutive
+    n = min(n, total);          // every run has a position, so those that share a unit are consecutive
     w.n = n;
     w.total = total;
     w.x0 = c < n ? static_cast<int>(static_cast<long long>(total) * c / n) : 0;
     w.x1 = c < n ? static_cast<int>(static_cast<long long>(total) * (c + 1) / n) : 0;
-    w.b = w.hr = w.at = w.len = w.t0 = w.t1 = 0;
+    w.b = w.h = w.at = w.len = w.t0 = w.t1 = 0;
     w.tiles = 1;
     int at = 0;
     for (int b0 = 0; b0 < p.B && w.x0 < w.x1; b0 += 32) {
-        const int v = b0 + lane < p.B ? (seq_tiles(p, b0 + lane) + p.unit_cost) * p.HR : 0;
+        const int v = b0 + lane < p.B ? (seq_tiles(p, b0 + lane) + p.unit_cost) * p.Hkv : 0;
         int incl = v;
         for (int k = 1; k < 32; k <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, k);
@@ -256,8 +259,8 @@ __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int 
             w.at = __shfl_sync(0xffffffffu, at + incl - v, src);
             w.b = b0 + src;
             w.enter(p);
-            w.hr = (w.x0 - w.at) / (w.tiles + p.unit_cost);
-            w.at += w.hr * (w.tiles + p.unit_cost);
+            w.h = (w.x0 - w.at) / (w.tiles + p.unit_cost);
+            w.at += w.h * (w.tiles + p.unit_cost);
             break;
         }
         at += __shfl_sync(0xffffffffu, incl, 31);
@@ -359,7 +362,9 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         fence_mbar_init();
     }
     grid_launch_dependents();
-    Walk w = find_run(p, static_cast<int>(blockIdx.x), static_cast<int>(gridDim.x), lane);
+    const int run = static_cast<int>(blockIdx.x) / p.RB, rb = static_cast<int>(blockIdx.x) - run * p.RB;
+    const int row0 = rb * (8 * NT);                 // the CTA's first query row of every K/V head
+    Walk w = find_run(p, run, static_cast<int>(gridDim.x) / p.RB, lane);
     bool more = w.settle(p);
     __syncthreads();
 
@@ -373,7 +378,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         uint32_t phase = 1u;               // the first pass over the ring waits for nothing
         bool ok = true;
         for (; more && ok; w.step(p), more = w.settle(p), ++unit) {
-            const int hkv = w.hr / p.RB, bkv = w.b * p.Hkv + hkv;
+            const int bkv = w.b * p.Hkv + w.h;
             for (int i = w.t0; i < w.t1; ++i) {
                 ok = __all_sync(0xffffffffu, mbar_wait(&empty[st], phase, abort_flag, kCdSiteEmpty));
                 if (!ok) break;
@@ -410,8 +415,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     ok = __all_sync(0xffffffffu,
                                     mbar_wait(&q_empty[buf], ((unit >> 1) & 1) ^ 1, abort_flag, kCdSiteEmpty));
                     if (!ok) break;
-                    q_fragments<D, kFmt, NT>(p, smem, buf, static_cast<size_t>(bkv) * (p.G * p.Nq),
-                                             (w.hr - hkv * p.RB) * (8 * NT), lane);
+                    q_fragments<D, kFmt, NT>(p, smem, buf, static_cast<size_t>(bkv) * (p.G * p.Nq), row0, lane);
                     mbar_arrive(&q_full[buf]);
                 }
             }
@@ -451,9 +455,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     // or outputs, so that the barriers below stay matched.
     for (; more; w.step(p), more = w.settle(p)) {
         // ---- one unit, or the CTA's part of it
-        const int hkv = w.hr / p.RB;
-        const int row0 = (w.hr - hkv * p.RB) * (8 * NT);
-        const size_t rows_at = static_cast<size_t>(w.b * p.Hkv + hkv) * R;   // first query row of the K/V head
+        const size_t rows_at = static_cast<size_t>(w.b * p.Hkv + w.h) * R;   // first query row of the K/V head
         const int buf = unit & 1;
         ok = ok && mbar_wait(&q_full[buf], (unit >> 1) & 1, abort_flag, kCdSiteFull);
         ok = __all_sync(0xffffffffu, ok);
@@ -691,8 +693,8 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
         if (w.t0 == 0 && threadIdx.x == 0) {
             const long long end = w.at + p.unit_cost + w.tiles;                      // past the last tile
-            const int last = static_cast<int>((end * w.n - 1) / w.total);            // its CTA
-            p.meta[w.b * p.HR + w.hr] = make_int2(whole ? -1 : slot, last);
+            const int last = static_cast<int>((end * w.n - 1) / w.total);            // its run
+            p.meta[(w.b * p.Hkv + w.h) * p.RB + rb] = make_int2(whole ? -1 : slot, last - run + 1);
         }
         constexpr int kPitch = L::kCols + 4;
         // 16 threads a row, kCols / 16 columns each
@@ -794,10 +796,10 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
     const int b = bkv / p.Hkv, hkv = bkv - b * p.Hkv;
     const int rb = r / p.rows_cta, in = r - rb * p.rows_cta;
     grid_wait();                                      // the main kernel's results, and the prefix's
-    const int2 meta = p.meta[b * p.HR + hkv * p.RB + rb];
+    const int2 meta = p.meta[bkv * p.RB + rb];
     const bool whole = meta.x < 0;
     if (whole && f.n_cta == 0) return;                // written by the main kernel
-    const int own = whole ? 1 : meta.y - (meta.x >> 1) + 1;
+    const int own = whole ? 1 : meta.y;
     // the prefix unit that holds the row, and the CTAs that share it
     int np = 0, pin = 0;
     size_t pslot = 0;
@@ -808,8 +810,8 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
         const long long total = static_cast<long long>(f.Hkv) * f.n_rowtiles * f.n_tiles;
         const long long ts = static_cast<long long>(pu) * f.n_tiles;
         const int first = static_cast<int>(((ts + 1) * f.n_cta - 1) / total);
-        np = (static_cast<int>(((ts + f.n_tiles) * f.n_cta - 1) / total) - first + 1) * f.subs;
-        pslot = static_cast<size_t>(first + pu) * f.subs;
+        np = static_cast<int>(((ts + f.n_tiles) * f.n_cta - 1) / total) - first + 1;
+        pslot = static_cast<size_t>(first + pu);
     }
     const int n = own + np;
     float M = -INFINITY, Z = 0.f, acc[kPer];
@@ -829,7 +831,7 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
                 o = p.o_unit + static_cast<size_t>(gr) * D;
                 lse = p.lse_unit[gr];
             } else {
-                prow = static_cast<size_t>(s == 0 ? meta.x : 2 * ((meta.x >> 1) + s)) * p.rows_cta + in;
+                prow = static_cast<size_t>(s == 0 ? meta.x : 2 * ((meta.x >> 1) + s * p.RB)) * p.rows_cta + in;
                 o = p.o_part + prow * D;
                 lse = p.lse_part[prow];
             }

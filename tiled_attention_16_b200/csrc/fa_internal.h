@@ -251,9 +251,9 @@ struct CacheDecodeParams {
     float *o_part, *lse_part;  // parts of units shared by CTAs: slots 2 c, 2 c + 1 of rows_cta rows each
     float *o_unit, *lse_unit;  // [B*Hq*Nq, D], [B*Hq*Nq]: undivided units' results for the merge with the
                                // prefix (null without one: they go to o and lse)
-    int2* meta;              // [B * HR]: first slot (-1: undivided), last CTA of the unit
+    int2* meta;              // [B * Hkv * RB]: a unit's first slot (-1: undivided) and parts, for each row block
     int B, Hkv, G, Nq, capacity, causal;
-    int rows_cta, RB, HR;    // query rows a CTA holds (8 or 16), row blocks of a K/V head, Hkv * RB
+    int rows_cta, RB;        // query rows a CTA holds (8 or 16), row blocks of a K/V head
     int n_cta;
     int unit_cost;           // positions a unit counts besides its tiles
     float scale_log2;
@@ -265,14 +265,14 @@ int cache_decode_unit_cost(int rows_cta);
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
                                 const CacheDecodeParams& p, bool after_prefix, cudaStream_t stream);
 
-// Shared prefix (fa_prefix.cu).  A unit is rows_unit of the B * G * Nq rows of
-// a K/V head; the part of unit u that CTA c computes lies in slot c + u of
-// 256 rows: rows_unit rows of each of its `subs` partial results.
+// Shared prefix (fa_prefix.cu).  A unit is rows_unit (128 or 256) of the
+// B * G * Nq rows of a K/V head; the part of unit u that CTA c computes lies in
+// slot c + u of rows_unit rows.
 struct PrefixParams {
     const void* q;
     float *o_part, *lse_part;
     int B, Hkv, G, Nq, Np;
-    int rows_unit, subs, n_rowtiles, n_tiles;
+    int rows_unit, n_rowtiles, n_tiles;
     int n_cta;               // 0: no prefix
     float scale_log2;
 };

@@ -14,8 +14,8 @@
 // exponentials are taken:
 //   kRows2    a unit is 256 rows and both blocks use the same key tile (three
 //             quarters of the shared-memory fill per product)
-//   otherwise a unit is 128 rows, the blocks take alternate key tiles, and the
-//             two partial results of a part stay apart until the combine
+//   otherwise a unit is 128 rows, the blocks take alternate key tiles, and their
+//             two accumulators are joined as they leave tensor memory
 // Up to 128 rows the work is bound by HBM whichever rows are real: a 64 KB
 // key tile costs about 1000 tensor cycles and, at the copy rate, 2800 cycles.
 //
@@ -46,10 +46,12 @@ struct PfLayout {
     static constexpr int kQ = 0;
     static constexpr int kK = kQ + kQTiles * kTileBytes;
     static constexpr int kV = kK + kStages * kTileBytes;
-    static constexpr int kBar = kV + kStages * kTileBytes;
-    static constexpr int kMisc = kBar + (1 + 2 * kStages + 2 + 2 + 1 + 1) * 8;
+    static constexpr int kMl = kV + kStages * kTileBytes;              // two floats a row
+    static constexpr int kBar = kMl + (kRows2 ? 0 : kTileM * 8);
+    static constexpr int kMisc = kBar + (1 + 2 * kStages + 2 + 2 + 1 + 1 + 3) * 8;
     static constexpr int kBytes = kMisc + 16;
     static constexpr int kAlloc = kBytes + 1024;
+    static_assert(kAlloc <= 227 * 1024, "one CTA must fit");
 };
 
 __device__ __forceinline__ float pf_lg2(float x) {
@@ -100,6 +102,9 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
     uint64_t* p_full = s_full + 2;           // [2]
     uint64_t* part_done = p_full + 2;        // every MMA of the part has completed
     uint64_t* drain = part_done + 1;
+    uint64_t* ml_full = drain + 1;           // alternate key tiles: (m, l) of block 1 are in place,
+    uint64_t* f_full = ml_full + 1;          // the factors of both accumulators are,
+    uint64_t* o_read = f_full + 1;           // both accumulators have been read
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
 
@@ -117,6 +122,9 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         }
         mbar_init(part_done, 1);
         mbar_init(drain, 1);
+        mbar_init(ml_full, kTileM);
+        mbar_init(f_full, kTileM);
+        mbar_init(o_read, 2 * kTileM);
         *abort_flag = 0;
         fence_mbar_init();
     }
@@ -346,41 +354,83 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
             if (more) load_q(w.u);
             const int hkv = done.u / p.n_rowtiles;
             const int row = (done.u - hkv * p.n_rowtiles) * p.rows_unit + (kRows2 ? s * kTileM : 0) + r;
-            const size_t prow = static_cast<size_t>(blockIdx.x + done.u) * 256 + s * kTileM + r;
+            const size_t prow = static_cast<size_t>(blockIdx.x + done.u) * p.rows_unit + (kRows2 ? s * kTileM : 0) + r;
             const bool valid = row < n_rows;
-            if (n_here > 0) {
-                // 8 columns of 8 rows a store, whole 32-byte sectors
-                const float inv_l = 1.f / l;
-                const int row_w = row - lane;                          // the warp's first row
-                float* out = p.o_part + (prow - lane) * D;
+            // Factors of this row's accumulators.  With alternate key tiles both blocks
+            // hold part of the same rows (the second nothing, when the part is one key
+            // tile); a warp reaches the other block's accumulator of its rows too, so
+            // each warpgroup joins half of the columns.
+            float f0 = 1.f / l, f1 = 0.f, lse;
+            const bool join = !kRows2 && done.n > 1;
+            if constexpr (kRows2) {
+                lse = (m_used + pf_lg2(l)) * 0.69314718055994531f;
+            } else {
+                // block 1 hands (m, l) over and gets the factors back
+                float2* ml = reinterpret_cast<float2*>(smem + L::kMl) + r;
+                const uint32_t parity = (parts - 1) & 1;
+                if (s == 1) {
+                    *ml = make_float2(m_used, l);
+                    mbar_arrive(ml_full);
+                    ok = mbar_wait(f_full, parity, abort_flag, kPfO);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    const float2 f = *ml;
+                    f0 = f.x;
+                    f1 = f.y;
+                    lse = 0.f;
+                } else {
+                    ok = mbar_wait(ml_full, parity, abort_flag, kPfO);
+                    if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+                    const float2 o1 = *ml;
+                    const float M = join ? fmaxf(m_used, o1.x) : m_used;
+                    const float w0 = ex2(m_used - M), w1 = join ? ex2(o1.x - M) : 0.f;   // NaN stays NaN
+                    const float ls = join ? w0 * l + w1 * o1.y : l;
+                    f0 = w0 / ls;
+                    f1 = w1 / ls;
+                    lse = (M + pf_lg2(ls)) * 0.69314718055994531f;
+                    *ml = make_float2(f0, f1);
+                    mbar_arrive(f_full);
+                }
+            }
+            // 8 columns of 8 rows a store, whole 32-byte sectors
+            const int row_w = row - lane;                          // the warp's first row
+            float* out = p.o_part + (prow - lane) * D;
+            const uint32_t t0 = kRows2 ? tO : tmem + lane_off + 256;
 #pragma unroll 1
-                for (int half = 0; half < 2; ++half) {
-                    const int ra = half * 16 + (lane >> 2), rb = ra + 8;
-                    const float ia = __shfl_sync(0xffffffffu, inv_l, ra), ib = __shfl_sync(0xffffffffu, inv_l, rb);
-                    const bool va = row_w + ra < n_rows, vb = row_w + rb < n_rows;
+            for (int half = 0; half < 2; ++half) {
+                const int ra = half * 16 + (lane >> 2), rb = ra + 8;
+                const float a0 = __shfl_sync(0xffffffffu, f0, ra), b0 = __shfl_sync(0xffffffffu, f0, rb);
+                const float a1 = __shfl_sync(0xffffffffu, f1, ra), b1 = __shfl_sync(0xffffffffu, f1, rb);
+                const bool va = row_w + ra < n_rows, vb = row_w + rb < n_rows;
+                constexpr int kQ = kRows2 ? D / 32 : D / 64;       // blocks of 32 columns
 #pragma unroll 1
-                    for (int q = 0; q < D / 32; ++q) {
-                        uint32_t ov[16];
-                        tmem_ld_16x32(tO + (static_cast<uint32_t>(half * 16) << 16) + q * 32, ov);
-                        tmem_ld_wait();
+                for (int q = 0; q < kQ; ++q) {
+                    const int col = (kRows2 ? 0 : s * (D / 2)) + q * 32;
+                    uint32_t ov[16], pv[16];
+                    tmem_ld_16x32(t0 + (static_cast<uint32_t>(half * 16) << 16) + col, ov);
+                    if (join) tmem_ld_16x32(t0 + 128 + (static_cast<uint32_t>(half * 16) << 16) + col, pv);
+                    tmem_ld_wait();
 #pragma unroll
-                        for (int c8 = 0; c8 < 4; ++c8) {
-                            const int d = q * 32 + c8 * 8 + (lane & 3) * 2;
-                            if (va)
-                                *reinterpret_cast<float2*>(out + static_cast<size_t>(ra) * D + d) =
-                                    make_float2(__uint_as_float(ov[4 * c8]) * ia, __uint_as_float(ov[4 * c8 + 1]) * ia);
-                            if (vb)
-                                *reinterpret_cast<float2*>(out + static_cast<size_t>(rb) * D + d) =
-                                    make_float2(__uint_as_float(ov[4 * c8 + 2]) * ib,
-                                                __uint_as_float(ov[4 * c8 + 3]) * ib);
+                    for (int c8 = 0; c8 < 4; ++c8) {
+                        const int d = col + c8 * 8 + (lane & 3) * 2;
+                        float v[4];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            v[e] = __uint_as_float(ov[4 * c8 + e]) * (e < 2 ? a0 : b0);
+                            if (join) v[e] = fmaf(__uint_as_float(pv[4 * c8 + e]), e < 2 ? a1 : b1, v[e]);
                         }
+                        if (va) *reinterpret_cast<float2*>(out + static_cast<size_t>(ra) * D + d) = make_float2(v[0], v[1]);
+                        if (vb) *reinterpret_cast<float2*>(out + static_cast<size_t>(rb) * D + d) = make_float2(v[2], v[3]);
                     }
                 }
-                if (valid) p.lse_part[prow] = (m_used + pf_lg2(l)) * 0.69314718055994531f;
-            } else if (valid) {
-                p.lse_part[prow] = -INFINITY;   // this block had no key tile
             }
+            if (valid && (kRows2 || s == 0)) p.lse_part[prow] = lse;
             tc_fence_before();
+            if constexpr (!kRows2) {
+                // the next part overwrites both accumulators
+                mbar_arrive(o_read);
+                ok = mbar_wait(o_read, (parts - 1) & 1, abort_flag, kPfO);
+                if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
+            }
         }
     }
 
@@ -406,7 +456,7 @@ cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams&
 
 cudaError_t launch_prefix(int D, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& p,
                           cudaStream_t stream) {
-    if (p.subs == 1) return D == 128 ? go<128, true>(tk, tv, p, stream) : go<64, true>(tk, tv, p, stream);
+    if (p.rows_unit == 2 * kTileM) return D == 128 ? go<128, true>(tk, tv, p, stream) : go<64, true>(tk, tv, p, stream);
     return D == 128 ? go<128, false>(tk, tv, p, stream) : go<64, false>(tk, tv, p, stream);
 }
 
