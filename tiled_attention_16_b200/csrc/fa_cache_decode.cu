@@ -198,7 +198,7 @@ __device__ __forceinline__ int seq_tiles(const CacheDecodeParams& p, int b) {
 // [total c / n, total (c + 1) / n).  With more query rows a K/V head than a CTA
 // holds, RB CTAs take a run, one a block of rows, at the same time: the tiles
 // come from HBM once and from L2 for the others (8 sequences of 32K slots, 32
-// rows a head: 174 us with the row blocks as units of their own).
+// rows a head: 163 us, 174 with the row blocks as units of their own).
 struct Walk {
     int x0, x1, total, n;       // the run's positions, all positions, runs with any
     int b, h, at, tiles, len;   // unit, its first position, its tiles, its sequence's length
@@ -231,9 +231,20 @@ struct Walk {
     }
 };
 
-// Warp-wide: run c of n, at the unit its positions begin in.
+// Warp-wide: run c of n, at the unit its positions begin in; or, where units
+// are not divided, unit c.
 __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int n, int lane) {
     Walk w;
+    if (p.undivided) {
+        w.b = c / p.Hkv;
+        w.h = c - w.b * p.Hkv;
+        w.enter(p);
+        w.at = w.x0 = 0;
+        w.x1 = w.total = w.tiles + p.unit_cost;
+        w.n = 1;
+        w.t0 = w.t1 = 0;
+        return w;
+    }
     int total = 0;
 #pragma unroll 4
     for (int b = lane; b < p.B; b += 32) total += (seq_tiles(p, b) + p.unit_cost) * p.Hkv;
@@ -694,7 +705,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         if (w.t0 == 0 && threadIdx.x == 0) {
             const long long end = w.at + p.unit_cost + w.tiles;                      // past the last tile
             const int last = static_cast<int>((end * w.n - 1) / w.total);            // its run
-            p.meta[(w.b * p.Hkv + w.h) * p.RB + rb] = make_int2(whole ? -1 : slot, last - run + 1);
+            p.meta[(w.b * p.Hkv + w.h) * p.RB + rb] = make_int2(whole ? -1 : slot, whole ? 1 : last - run + 1);
         }
         constexpr int kPitch = L::kCols + 4;
         // 16 threads a row, kCols / 16 columns each

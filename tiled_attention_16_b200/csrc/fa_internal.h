@@ -256,6 +256,7 @@ struct CacheDecodeParams {
     int rows_cta, RB;        // query rows a CTA holds (8 or 16), row blocks of a K/V head
     int n_cta;
     int unit_cost;           // positions a unit counts besides its tiles
+    int undivided;           // every unit is a run
     float scale_log2;
 };
 // CTAs of the cache part that fit on an SM at once (shared memory and registers).
