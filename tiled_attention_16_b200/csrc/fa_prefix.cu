@@ -176,9 +176,14 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
         if (lane == 0) {
             constexpr uint32_t kIdS = idesc_bf16_f32(kTileM, kTileN, 0, 0);
             constexpr uint32_t kIdPV = idesc_bf16_f32(kTileM, D, 0, 1);
-            const uint32_t q_base = smem_u32(smem + L::kQ);
-            const uint32_t k_base = smem_u32(smem + L::kK);
-            const uint32_t v_base = smem_u32(smem + L::kV);
+            // Descriptors of the first k-step; the others are a constant number of
+            // 16-byte units on, added to the address field (this thread shares its
+            // scheduler with softmax warps, so every instruction between two MMAs
+            // counts).
+            const uint64_t q_desc = sdesc_sw128(smem_u32(smem + L::kQ), 16, 1024);
+            const uint64_t k_desc = sdesc_sw128(smem_u32(smem + L::kK), 16, 1024);
+            const uint64_t v_desc = sdesc_sw128(smem_u32(smem + L::kV), L::kAtomBytes, 1024);
+            constexpr uint32_t kTileUnits = L::kTileBytes / 16;
             bool ok = true;
             int gk = 0;         // key tiles of earlier parts
             int waited = 0;     // key tiles whose arrival has been waited for
@@ -192,12 +197,11 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     waited = G + 1;
                 }
                 tc_fence_after();
-                const uint32_t qa = q_base + (kRows2 ? s * L::kTileBytes : 0);
-                const uint32_t ka = k_base + st * L::kTileBytes;
+                const uint64_t qa = q_desc + (kRows2 ? s * kTileUnits : 0), ka = k_desc + st * kTileUnits;
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t off = (kk >> 2) * L::kAtomBytes + (kk & 3) * 32;
-                    mma_ss(tmem + s * 128, sdesc_sw128(qa + off, 16, 1024), sdesc_sw128(ka + off, 16, 1024), kIdS, kk > 0);
+                    const uint32_t off = ((kk >> 2) * L::kAtomBytes + (kk & 3) * 32) / 16;
+                    mma_ss(tmem + s * 128, qa + off, ka + off, kIdS, kk > 0);
                 }
                 tc_commit(&s_full[s]);
                 return true;
@@ -212,11 +216,10 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     if (!(ok = mbar_wait(&p_full[s], np[s] & 1, abort_flag, kPfP))) break;
                     ++np[s];
                     tc_fence_after();
-                    const uint32_t va = v_base + st * L::kTileBytes;
+                    const uint64_t va = v_desc + st * kTileUnits;
 #pragma unroll
                     for (int kk = 0; kk < kTileN / 16; ++kk)
-                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8,
-                               sdesc_sw128(va + kk * 2048, L::kAtomBytes, 1024), kIdPV, (i > 1 || kk > 0));
+                        mma_ts(tmem + 256 + s * 128, tmem + s * 128 + kk * 8, va + kk * (2048 / 16), kIdPV, (i > 1 || kk > 0));
                     if (i % kTileSteps == kTileSteps - 1) tc_commit(&kv_empty[st]);
                     if (i + 2 < n_steps) ok = issue_s(i + 2);
                 }
