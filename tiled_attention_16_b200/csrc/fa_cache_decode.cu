@@ -66,11 +66,10 @@ struct CdLayout {
     static constexpr int kQ = kScales + 2 * kStages * kScaleBytes;      // two units' fragments,
     static constexpr int kQScale = kQ + 2 * kQFrag;                     // and their rows' factors
     static constexpr int kMerge = kQScale + 2 * NT * 8 * 4;             // [4 warps][8 rows][kCols + 4] fp32
-    static constexpr int kCols = kWide ? (NT == 1 ? 64 : 32) : (NT == 1 ? D : 64);
+    static constexpr int kCols = kWide ? (NT == 1 ? 64 : 32) : D;       // a round of the join: 0.7 us
     static constexpr int kMl = kMerge + 4 * 8 * (kCols + 4) * 4;        // m, l and V exponent of the warps
     static constexpr int kBar = kMl + 4 * 40 * 4;
-    static constexpr int kBytes = kBar + (2 * kStages + 4) * 8 + 16;
-    static constexpr int kAlloc = kBytes + 1024;
+    static constexpr int kAlloc = kBar + (2 * kStages + 4) * 8 + 16;
     static_assert((kAlloc + 1024) * kCtas <= 228 * 1024, "CTAs must fit");
 };
 
@@ -235,6 +234,7 @@ struct Walk {
 // are not divided, unit c.
 __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int n, int lane) {
     Walk w;
+    auto weight = [&](int b) { return b < p.B ? (seq_tiles(p, b) + p.unit_cost) * p.Hkv : 0; };
     if (p.undivided) {
         w.b = c / p.Hkv;
         w.h = c - w.b * p.Hkv;
@@ -245,9 +245,10 @@ __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int 
         w.t0 = w.t1 = 0;
         return w;
     }
-    int total = 0;
+    const int first = weight(lane);
+    int total = first;
 #pragma unroll 4
-    for (int b = lane; b < p.B; b += 32) total += (seq_tiles(p, b) + p.unit_cost) * p.Hkv;
+    for (int b = lane + 32; b < p.B; b += 32) total += weight(b);
     total = __reduce_add_sync(0xffffffffu, total);
     n = min(n, total);          // every run has a position, so those that share a unit are consecutive
     w.n = n;
@@ -258,7 +259,7 @@ __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int 
     w.tiles = 1;
     int at = 0;
     for (int b0 = 0; b0 < p.B && w.x0 < w.x1; b0 += 32) {
-        const int v = b0 + lane < p.B ? (seq_tiles(p, b0 + lane) + p.unit_cost) * p.Hkv : 0;
+        const int v = b0 == 0 ? first : weight(b0 + lane);
         int incl = v;
         for (int k = 1; k < 32; k <<= 1) {
             const int o = __shfl_up_sync(0xffffffffu, incl, k);
@@ -303,20 +304,33 @@ __device__ __forceinline__ void q_fragments(const CacheDecodeParams& p, uint8_t*
     const int g8 = lane >> 2, t4 = lane & 3, R = p.G * p.Nq;
     uint2* frag = reinterpret_cast<uint2*>(smem + L::kQ + buf * L::kQFrag) + lane;
     float* factor = reinterpret_cast<float*>(smem + L::kQScale) + buf * NT * 8;
+    uint2 raw[NT][kSteps];   // all loads before the first use
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int r = row0 + n * 8 + g8;
         const __nv_bfloat16* qrow = reinterpret_cast<const __nv_bfloat16*>(p.q) + (rows_at + (r < R ? r : 0)) * D;
+#pragma unroll
+        for (int s = 0; s < kSteps; ++s) {
+            raw[n][s] = make_uint2(0u, 0u);
+            if (r < R) {
+                if constexpr (kFmt != 0) {
+                    // step s = 4 hh + w4: values (chunk of 16) * 16 + 4 w4 .. + 3
+                    const int d = (D == 128 ? (2 * t4 + (s >> 2)) : t4) * 16 + (s & 3) * 4;
+                    raw[n][s] = __ldg(reinterpret_cast<const uint2*>(qrow + d));
+                } else {
+                    const uint32_t* at = reinterpret_cast<const uint32_t*>(qrow + s * 16 + 2 * t4);
+                    raw[n][s] = make_uint2(__ldg(at), __ldg(at + 4));
+                }
+            }
+        }
+    }
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
         if constexpr (kFmt != 0) {
-            uint2 raw[kSteps];
             uint32_t am = 0u;
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                // step s = 4 hh + w4: values (chunk of 16) * 16 + 4 w4 .. + 3
-                const int d = (D == 128 ? (2 * t4 + (s >> 2)) : t4) * 16 + (s & 3) * 4;
-                raw[s] = r < R ? __ldg(reinterpret_cast<const uint2*>(qrow + d)) : make_uint2(0u, 0u);
-                am = __vmaxu2(am, __vmaxu2(raw[s].x & 0x7fff7fffu, raw[s].y & 0x7fff7fffu));
-            }
+            for (int s = 0; s < kSteps; ++s)
+                am = __vmaxu2(am, __vmaxu2(raw[n][s].x & 0x7fff7fffu, raw[n][s].y & 0x7fff7fffu));
             am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 1));
             am = __vmaxu2(am, __shfl_xor_sync(0xffffffffu, am, 2));
             // 2^(14 - exponent of the row's largest value); q = 0: any
@@ -324,17 +338,16 @@ __device__ __forceinline__ void q_fragments(const CacheDecodeParams& p, uint8_t*
             const int f = min(max(14 - ex, -113), 126);
             const float up = __int_as_float((127 + f) << 23);
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s)
+            for (int s = 0; s < kSteps; ++s) {
+                const uint2 w = raw[n][s];
                 frag[(n * kSteps + s) * 32] =
-                    make_uint2(pack_half2(__uint_as_float(raw[s].x << 16) * up, __uint_as_float(raw[s].x & 0xffff0000u) * up),
-                               pack_half2(__uint_as_float(raw[s].y << 16) * up, __uint_as_float(raw[s].y & 0xffff0000u) * up));
+                    make_uint2(pack_half2(__uint_as_float(w.x << 16) * up, __uint_as_float(w.x & 0xffff0000u) * up),
+                               pack_half2(__uint_as_float(w.y << 16) * up, __uint_as_float(w.y & 0xffff0000u) * up));
+            }
             if (t4 == 0) factor[n * 8 + g8] = pow2_inverse(up) * p.scale_log2;
         } else {
 #pragma unroll
-            for (int s = 0; s < kSteps; ++s) {
-                const uint32_t* at = reinterpret_cast<const uint32_t*>(qrow + s * 16 + 2 * t4);
-                frag[(n * kSteps + s) * 32] = r < R ? make_uint2(__ldg(at), __ldg(at + 4)) : make_uint2(0u, 0u);
-            }
+            for (int s = 0; s < kSteps; ++s) frag[(n * kSteps + s) * 32] = raw[n][s];
             if (t4 == 0) factor[n * 8 + g8] = p.scale_log2;
         }
     }
@@ -350,8 +363,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     constexpr int kStages = L::kStages;
     constexpr int kSteps = D / 16;
     constexpr float kShift = kHalf ? 6.f : 0.f;   // P is 2^kShift where the score is the row's (stale) maximum
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle's alignment
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
     uint64_t* empty = full + kStages;
     uint64_t* q_full = empty + kStages;    // [2]
@@ -360,6 +372,11 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 
     const int warp = threadIdx.x >> 5;
     const int lane = threadIdx.x & 31;
+    grid_launch_dependents();
+    const int run = static_cast<int>(blockIdx.x) / p.RB, rb = static_cast<int>(blockIdx.x) - run * p.RB;
+    const int row0 = rb * (8 * NT);                 // the CTA's first query row of every K/V head
+    Walk w = find_run(p, run, static_cast<int>(gridDim.x) / p.RB, lane);
+    bool more = w.settle(p);
     if (threadIdx.x == 0) {
         for (int s = 0; s < kStages; ++s) {
             mbar_init(&full[s], 1);
@@ -372,11 +389,6 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         *abort_flag = 0;
         fence_mbar_init();
     }
-    grid_launch_dependents();
-    const int run = static_cast<int>(blockIdx.x) / p.RB, rb = static_cast<int>(blockIdx.x) - run * p.RB;
-    const int row0 = rb * (8 * NT);                 // the CTA's first query row of every K/V head
-    Walk w = find_run(p, run, static_cast<int>(gridDim.x) / p.RB, lane);
-    bool more = w.settle(p);
     __syncthreads();
 
     if (warp == 4) {
