@@ -61,7 +61,8 @@ def ints(*x):
 # ---------------------------------------------------------------- write, read
 
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
-@pytest.mark.parametrize("B,H,N,cap,D", [(1, 1, 1, 4, 128), (3, 2, 5, 64, 64), (2, 3, 67, 132, 128), (4, 8, 33, 40, 64)])
+@pytest.mark.parametrize("B,H,N,cap,D", [(1, 1, 1, 4, 128), (3, 2, 5, 64, 64), (2, 3, 67, 132, 128), (4, 8, 33, 40, 64),
+                                         (2, 40, 1, 8, 128), (1, 100, 1, 4, 64), (2, 33, 3, 12, 128), (1, 17, 130, 200, 64)])
 def test_write_then_read(fmt, B, H, N, cap, D):
     dev = _gpu()
     kc, vc, ks, vs = new_cache(B, H, cap, D, fmt, dev)
@@ -257,6 +258,9 @@ PREFIX = [
     (33, 8, 2, 2, 32, 64, 700, [b % 33 for b in range(33)]),    # 264 rows: three tiles, the last nearly empty
     (4, 32, 8, 1, 132, 128, 4100, [1, 130, 50, 90]),
     (2, 2, 1, 1, 64, 64, 40000, [64, 0]),
+    (1, 100, 100, 1, 4, 64, 2600, [3]),                         # one row tile each: CTAs begin and end inside heads
+    (130, 16, 16, 1, 4, 128, 2000, [b % 5 for b in range(130)]),   # the same with two
+    (300, 64, 32, 2, 4, 64, 200, [1] * 300),                    # more (head, row tile) pairs than CTAs
 ]
 
 
@@ -340,6 +344,104 @@ def test_repeated_calls_and_streams_are_bitwise_equal():
                 res.append(cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv))
     torch.cuda.synchronize()
     assert all(torch.equal(r[0], want[0]) and torch.equal(r[1], want[1]) for r in res)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3"])
+@pytest.mark.parametrize("Np", [0, 1500])
+def test_captured_calls_replay(fmt, Np):
+    """A divided decode (and one behind a prefix) captured with its own
+    workspace: replays follow lengths, queries and cache, and stay right when
+    two graphs and eager calls are mixed."""
+    dev = _gpu()
+    B, Hq, Hkv, D, cap = 3, 8, 2, 128, 2000
+    kc, vc, ks, vs = filled(B, Hkv, cap, D, fmt, [cap] * B, dev)
+    q, lens = rows(B, Hq, 1, D, 3), ints(1, 700, 1999)
+    pk, pv = ((rows(1, Hkv, Np, D, 5)[0].contiguous(), rows(1, Hkv, Np, D, 6)[0].contiguous()) if Np else (None, None))
+    want = lambda: cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv)  # noqa: E731
+    want()
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            res = want()
+        graphs.append((g, res))
+    for step in range(4):
+        lens.copy_(ints(2000 - step, 64 * step, 333 * step))
+        q.copy_(rows(B, Hq, 1, D, 40 + step))
+        for g, res in graphs:
+            g.replay()
+        eager = want()
+        torch.cuda.synchronize()
+        for g, res in graphs:
+            assert torch.equal(res[0], eager[0]) and torch.equal(res[1], eager[1])
+    check_decode(q, kc, vc, ks, vs, lens, eager, pk=pk, pv=pv)
+
+
+@pytest.mark.parametrize("fmt,B,Hkv,cap", [("bf16", 3, 8, 1 << 20), ("e4m3", 2, 5, 1 << 23)])
+def test_offsets_past_32_bits(fmt, B, Hkv, cap):
+    """Caches of more than 2^32 bytes: rows written, read and attended to at
+    their far ends."""
+    dev = _gpu()
+    D, N, Hq = 128, 70, 2 * Hkv
+    kc, vc, ks, vs = cache.make_cache(B, Hkv, cap, D, FMT[fmt], dev)
+    assert kc.numel() * kc.element_size() > 1 << 32
+    for t in (kc, vc):
+        t.view(torch.uint8).zero_()
+    for t in (ks, vs):
+        if t is not None:
+            t.fill_(1.0)
+    k, v = rows(B, Hkv, N, D, 1), rows(B, Hkv, N, D, 2)
+    start = ints(*[cap - N - 3 * b for b in range(B)])
+    cache.cache_write(k, v, kc, vc, start, k_scale=ks, v_scale=vs)
+    b, h = B - 1, Hkv - 1
+    at = int(start[b])
+    ref = np64(k[b, h]) if fmt == "bf16" else so.quantise_rows(np64(k[b, h]), fmt)[0]
+    assert (np64(kc[b, h, at:at + N]) == ref).all() and not kc[b, h].view(torch.uint8)[:at].any()
+    q = (4 * rows(B, Hq, 1, D, 3).float()).to(torch.bfloat16)
+    lens = torch.zeros_like(start)
+    lens[b] = start[b] + N
+    o, lse = cache.decode_cache(q, kc, vc, lens, ks, vs)
+    assert A.device_status(dev) == A.FA_OK
+    # keys before `at` are zero: each has the score 0 and the value 0
+    kk, vv = (np64(c[b, :, at:at + N]) * (1 if s is None else np64(s[b, :, at:at + N])[..., None])
+              for c, s in ((kc, ks), (vc, vs)))
+    for head in (0, Hq - 1):
+        s = kk[head // 2] @ np64(q[b, head, 0]) * D ** -0.5
+        total = np.log(at + np.exp(s).sum())
+        ref = np.exp(s - total) @ vv[head // 2]
+        assert abs(float(lse[b, head, 0]) - total) <= 1e-4
+        wt = np.exp(s - total) @ np.abs(vv[head // 2])
+        assert (np.abs(np64(o[b, head, 0]) - ref) <= 1e-2 * wt + 1e-6).all()
+    assert torch.isneginf(lse[0]).all() and (o[0] == 0).all()
+    del kc, vc, ks, vs
+    torch.cuda.empty_cache()
+
+
+def test_refusals_on_the_gpu():
+    """What only the binding or a device pointer can show wrong."""
+    dev = _gpu()
+    kc, vc, ks, vs = filled(1, 1, 64, 64, "int8", [64], dev)
+    q, lens, k = rows(1, 1, 1, 64, 3), ints(64), rows(1, 1, 1, 64, 4)
+    for bad in (dict(k_scale=None), dict(v_scale=ks.double()), dict(workspace=torch.empty(1, device=dev).expand(1 << 30)),
+                dict(workspace=torch.empty(8, device=dev)), dict(prefix_k=k[0]), dict(scale=-1.0), dict(lse=ks),
+                dict(out=q.transpose(0, 1)[:, :, :, :32]), dict(prefix_k=k[0], prefix_v=k[0, :, :, :32])):
+        with pytest.raises((TypeError, ValueError, A.FAError)):
+            cache.decode_cache(q, kc, vc, lens, **{**dict(k_scale=ks, v_scale=vs), **bad})
+    for args in ((q.float(), kc, vc, lens), (q, kc.float(), vc, lens), (q, kc, vc[:, :, :32], lens),
+                 (q, kc, vc, lens.long()), (q[..., ::2], kc, vc, lens), (q, kc, vc, lens.cpu())):
+        with pytest.raises((TypeError, ValueError, A.FAError)):
+            cache.decode_cache(*args, k_scale=ks, v_scale=vs)
+    for args in ((k.float(), k), (k[..., ::2], k), (k, k[:, :, :, :32]), (k.cpu(), k)):
+        with pytest.raises((TypeError, ValueError, A.FAError)):
+            cache.cache_write(*args, kc, vc, lens, k_scale=ks, v_scale=vs)
+    with pytest.raises(A.FAError):
+        cache.cache_write(torch.empty(1, 1, 1, 68, device=dev, dtype=torch.bfloat16)[..., 4:], k, kc, vc, lens,
+                          k_scale=ks, v_scale=vs)       # 8-byte aligned
+    with pytest.raises(A.FAError):
+        cache.cache_read(kc, vc, 65, k_scale=ks, v_scale=vs)
+    cache.cache_write(k[:, :, :0], k[:, :, :0], kc, vc, lens, k_scale=ks, v_scale=vs)   # nothing to write
+    assert A.device_status(dev) == A.FA_OK
 
 
 def test_bf16_cache_agrees_with_decode():

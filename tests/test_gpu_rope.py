@@ -157,6 +157,67 @@ def test_gradient_against_differences():
         assert abs((np64(dw) * ew).sum() - num) <= 1e-5 * (1 + np.abs(np64(dw) * ew).sum())
 
 
+def test_offsets_past_32_bits():
+    """More than 2^31 elements: sampled rows against the definition."""
+    dev = _gpu()
+    N, Hq, Hkv, D = 150000, 112, 8, 128
+    g = torch.Generator(device=dev).manual_seed(3)
+    x = torch.empty(1, N, Hq + Hkv, D, device=dev, dtype=torch.bfloat16)
+    for i in range(0, N, 10000):
+        x[:, i:i + 10000] = torch.randn(1, 10000, Hq + Hkv, D, device=dev, generator=g, dtype=torch.float32)
+    q, k = x[:, :, :Hq].transpose(1, 2), x[:, :, Hq:].transpose(1, 2)
+    assert q.numel() > 1 << 31
+    w = torch.ones(D, device=dev)
+    inv = (10000.0 ** (-torch.arange(0, D, 2, dtype=torch.float64) / D)).float().to(dev)
+    oq, ok = rope.qk_norm_rope(q, k, w, w, inv)
+    dq, dk, dqw, dkw = rope.qk_norm_rope_bwd(oq, ok, q, k, w, w, inv)
+    for t, y, d, heads in ((q, oq, dq, (0, 57, Hq - 1)), (k, ok, dk, (0, Hkv - 1))):
+        for h in heads:
+            for n in (0, 77777, N - 1):
+                pos = np.array([[n]])
+                ref, u = so.norm_rope(np64(t[:, h:h + 1, n:n + 1]), np.ones(D), np64(inv), pos, 1e-6, False)
+                assert (np.abs(np64(y[0, h, n]) - ref[0, 0, 0]) <= BF * np.abs(ref[0, 0, 0]) * (1 + BF) + 1e-5).all()
+                rdx, _, sdx, _ = so.norm_rope_backward(np64(y[:, h:h + 1, n:n + 1]), np64(t[:, h:h + 1, n:n + 1]),
+                                                       np.ones(D), np64(inv), pos, 1e-6, False)
+                assert (np.abs(np64(d[0, h, n]) - rdx[0, 0, 0]) <= BF * np.abs(rdx[0, 0, 0]) * (1 + BF) + 1e-5 * sdx[0, 0, 0]).all()
+    # dy = y of the same rows, so g x r = x^2 r^2 (1 +- 2^-8): the sums are the rows' count, about
+    for dw, H in ((dqw, Hq), (dkw, Hkv)):
+        assert (np64(dw) / (N * H)).min() > 0.98 and (np64(dw) / (N * H)).max() < 1.02
+    del x, q, k, oq, ok, dq, dk
+    torch.cuda.empty_cache()
+
+
+def test_refusals_on_the_gpu():
+    q, k, qw, kw, inv, pos, dq, dk = make(1, 2, 1, 4, 64, 64, seed=2)
+    ok = dict(positions=pos)
+    for args, kwargs in (((q.float(), k, qw, kw, inv), ok), ((q[..., ::2], k[..., ::2], qw[:32], kw[:32], inv), ok),
+                         ((q, k, qw.half(), kw, inv), ok), ((q, k, qw, kw.bfloat16(), inv), ok),
+                         ((q, k, qw, kw, inv.double()), ok), ((q, k, qw, kw, inv), dict(positions=pos.long())),
+                         ((q, k, qw, kw, inv), dict(positions=pos[:, :2])), ((q, k, qw, kw, inv), dict(eps=0.0)),
+                         ((q, k, qw, kw, inv[:3]), ok), ((q, k[:, :, :3], qw, kw, inv), ok),
+                         ((q, k, qw, kw.cpu(), inv), ok), ((q, k, qw, kw, inv), dict(out_q=dq[:, :, :, :32]))):
+        with pytest.raises((TypeError, ValueError, A.FAError)):
+            rope.qk_norm_rope(*args, **kwargs)
+    wide = torch.empty(1, 1, 4, 64, device=q.device, dtype=torch.bfloat16)
+    for bad in (dict(dq=wide.expand(1, 2, 4, 64)), dict(workspace=torch.empty(8, device=q.device)),
+                dict(workspace=torch.empty(1, device=q.device).expand(1 << 30)), dict(dk=dk.float())):
+        with pytest.raises((TypeError, ValueError, A.FAError)):
+            rope.qk_norm_rope_bwd(dq, dk, q, k, qw, kw, inv, **bad)
+    assert A.device_status(q.device) == A.FA_OK
+
+
+def test_broadcast_inputs():
+    """Views whose rows repeat (stride 0) are read like any other."""
+    q, k, qw, kw, inv, pos, dq, dk = make(2, 4, 2, 9, 128, 64, seed=4)
+    qe, ke = q[:, :1].expand(-1, 4, -1, -1), k[:1].expand(2, -1, -1, -1)
+    a = rope.qk_norm_rope(qe, ke, qw, kw, inv, positions=pos)
+    b = rope.qk_norm_rope(qe.contiguous(), ke.contiguous(), qw, kw, inv, positions=pos)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    ga = rope.qk_norm_rope_bwd(dq, dk, qe, ke, qw, kw, inv, positions=pos)
+    gb = rope.qk_norm_rope_bwd(dq, dk, qe.contiguous(), ke.contiguous(), qw, kw, inv, positions=pos)
+    assert all(torch.equal(x, y) for x, y in zip(ga, gb))
+
+
 def test_graph_capture_and_other_stream():
     q, k, qw, kw, inv, pos, dq, dk = make(2, 4, 2, 65, 128, 128, seed=14)
     want = rope.qk_norm_rope(q, k, qw, kw, inv, positions=pos) + rope.qk_norm_rope_bwd(

@@ -227,8 +227,8 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if workspace is None:
         workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
     else:
-        if workspace.get_device() != index:
-            raise ValueError(f"all tensors must be on one device: got {q.device} and {workspace.device}")
+        if workspace.get_device() != index or not workspace.is_contiguous():
+            raise ValueError(f"workspace must be a contiguous buffer on {q.device}")
         nbytes = workspace.numel() * workspace.element_size()
     st = _cache_lib().fa_decode_cache(ctypes.byref(shp), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
                                       lens.data_ptr(), pk, pv, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),

@@ -223,12 +223,13 @@ cudaError_t cache_dispatch(int D, int fmt, F&& go) {
 }  // namespace
 
 cudaError_t launch_cache_write(int D, int fmt, CacheWriteParams p, cudaStream_t stream) {
-    const int rows = kCacheThreads / (D / 8) * kRows;
+    const int slots = kCacheThreads / (D / 8), rows = slots * kRows;
     // Heads of a tile: four for rows that lie token by token; and when there are
-    // fewer tokens than rows, as many as fill the tile.
+    // fewer tokens than rows, as many as fill the tile, but at most one a row slot
+    // (a thread's rows are tokens of one head).
     auto tiling = [&](const RopeRows& x, int& shift) {
         shift = p.H > 1 && p.N > 1 && x.stride_h < x.stride_n ? 2 : 0;
-        while ((rows >> shift) / 2 >= p.N && (1 << shift) < p.H) ++shift;
+        while ((rows >> shift) / 2 >= p.N && (1 << shift) < p.H && (2 << shift) <= slots) ++shift;
         const long long tn = rows >> shift, th = 1LL << shift;
         return p.B * ((p.N + tn - 1) / tn) * ((p.H + th - 1) / th);
     };

@@ -25,7 +25,7 @@ bool rows_ok(const fa_rows* r, int B, int H, int N) {
     const long long st[3] = {r->stride_b, r->stride_h, r->stride_n};
     const int n[3] = {B, H, N};
     for (int i = 0; i < 3; ++i)
-        if (n[i] > 1 && (st[i] < 0 || (st[i] & 7) != 0 || st[i] > (1LL << 44))) return false;
+        if (n[i] > 1 && (st[i] < 0 || (st[i] & 7) != 0 || st[i] > (1LL << 44) / n[i])) return false;
     return true;
 }
 

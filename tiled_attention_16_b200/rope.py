@@ -159,8 +159,8 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     dkw = torch.empty(D, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(_bwd_workspace(D, index), dtype=torch.uint8, device=dev)
-    elif workspace.get_device() != index:
-        raise ValueError(f"all tensors must be on one device: got {q.device} and {workspace.device}")
+    elif workspace.get_device() != index or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous buffer on {q.device}")
     st = L.fa_qk_norm_rope_bwd(ctypes.byref(shp), dq_out.data_ptr(), dk_out.data_ptr(), ctypes.byref(qr),
                                ctypes.byref(kr), qw, kw, freq, pos, ctypes.byref(dqr), ctypes.byref(dkr),
                                dqw.data_ptr(), dkw.data_ptr(), workspace.data_ptr(),
