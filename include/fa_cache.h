@@ -76,8 +76,10 @@ typedef struct {
     int causal;
 } fa_cache_decode_shape;
 
-/* Bytes of device workspace fa_decode_cache needs (0 if the shape is invalid
- * or there is no CUDA device). */
+/* Bytes of device workspace fa_decode_cache needs: 0 for caches of up to
+ * FA_CACHE_UNDIVIDED slots without a prefix (each sequence's head is one CTA's
+ * work there), and if the shape is invalid or there is no CUDA device. */
+#define FA_CACHE_UNDIVIDED 512
 FA_API size_t fa_decode_cache_workspace_bytes(const fa_cache_decode_shape* shape);
 
 /* q [B,Hq,Nq,D] bf16; the cache as above, with lens int32 [B] on the device
@@ -86,8 +88,9 @@ FA_API size_t fa_decode_cache_workspace_bytes(const fa_cache_decode_shape* shape
  * The prefix is read once for the whole batch: its rows of all sequences meet
  * it as one matrix.  The 8-bit formats multiply in fp16 on the codes (exact
  * there), q scaled by a power of two for each row; scales enter in fp32.
- * workspace: 256-byte aligned, contents on entry do not matter; calls that
- * may overlap need workspaces of their own.  Codes below a sequence's length
+ * workspace: 256-byte aligned (NULL allowed where 0 bytes are needed), contents
+ * on entry do not matter; calls that may overlap need workspaces of their own.
+ * Codes below a sequence's length
  * must be numbers (the writer's always are). */
 FA_API fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, const void* k_cache,
                                  const void* v_cache, const float* k_scale, const float* v_scale, const int* lens,

@@ -156,12 +156,15 @@ def test_decode_refusals():
         assert cache._cache_lib().fa_decode_cache_workspace_bytes(ctypes.byref(dshape(**kw))) == 0
     assert call_decode(dshape(D=96)) == UNSUP
     for kw in (dict(q=0), dict(q=P + 8), dict(kc=P + 4), dict(vc=0), dict(ks=0), dict(vs=P + 8), dict(lens=0),
-               dict(lens=P + 2), dict(o=0), dict(lse=0), dict(lse=P + 2), dict(ws=0), dict(ws=P + 128)):
+               dict(lens=P + 2), dict(o=0), dict(lse=0), dict(lse=P + 2)):
         assert call_decode(**kw) == BAD, kw
+    for kw in (dict(ws=0), dict(ws=P + 128)):       # caches up to 512 slots without a prefix need none
+        assert call_decode(dshape(capacity=516), **kw) == BAD and call_decode(dshape(n_prefix=5), pk=P, pv=P, **kw) == BAD
     assert call_decode(dshape(n_prefix=5)) == BAD and call_decode(dshape(n_prefix=5), pk=P, pv=P + 8) == BAD
     assert cache._cache_lib().fa_decode_cache_workspace_bytes(None) == 0
     if not torch.cuda.is_available():
         assert no_gpu(call_decode()) and no_gpu(call_decode(dshape(n_prefix=5), pk=P, pv=P))
+        assert no_gpu(call_decode(ws=0, nb=0)) and no_gpu(call_decode(dshape(capacity=512), ws=0, nb=0))
         assert no_gpu(call_decode(dshape(format=0, capacity=101), ks=0, vs=0))
 
 

@@ -167,14 +167,14 @@ def test_captured_write_follows_the_device_lengths():
     cache.cache_write(k, v, kc, vc, start, k_scale=ks, v_scale=vs)
     vc[1, :, :3], kc[1, :, :3] = 0, 0
     ks[1, :, :3], vs[1, :, :3] = 1, 1
-    ws = torch.empty(cache.decode_cache_workspace_bytes(2, 4, 2, 1, 16, 128, torch.float8_e4m3fn), device=dev, dtype=torch.uint8)
-    cache.decode_cache(q, kc, vc, start + 1, ks, vs, workspace=ws)
+    assert cache.decode_cache_workspace_bytes(2, 4, 2, 1, 16, 128, torch.float8_e4m3fn) == 0
+    cache.decode_cache(q, kc, vc, start + 1, ks, vs)
     torch.cuda.synchronize()
     lens = start + 1
     g = torch.cuda.CUDAGraph()
     with torch.cuda.graph(g):
         cache.cache_write(k, v, kc, vc, start, k_scale=ks, v_scale=vs)
-        o, lse = cache.decode_cache(q, kc, vc, lens, ks, vs, workspace=ws)
+        o, lse = cache.decode_cache(q, kc, vc, lens, ks, vs)
         start += 1
         lens += 1
     for step in range(5):
@@ -357,8 +357,13 @@ def test_captured_calls_replay(fmt, Np):
     kc, vc, ks, vs = filled(B, Hkv, cap, D, fmt, [cap] * B, dev)
     q, lens = rows(B, Hq, 1, D, 3), ints(1, 700, 1999)
     pk, pv = ((rows(1, Hkv, Np, D, 5)[0].contiguous(), rows(1, Hkv, Np, D, 6)[0].contiguous()) if Np else (None, None))
-    want = lambda: cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv)  # noqa: E731
-    want()
+    nbytes = cache.decode_cache_workspace_bytes(B, Hq, Hkv, 1, cap, D, FMT[fmt], Np)
+    ws = torch.empty(nbytes, device=dev, dtype=torch.uint8)
+    want = lambda **kw: cache.decode_cache(q, kc, vc, lens, ks, vs, pk, pv, **kw)  # noqa: E731
+    a, b = want(), want(workspace=ws)
+    assert nbytes > 0 and torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    with pytest.raises(A.FAError):
+        want(workspace=ws[256:])
     torch.cuda.synchronize()
     graphs = []
     for _ in range(2):
@@ -424,7 +429,7 @@ def test_refusals_on_the_gpu():
     kc, vc, ks, vs = filled(1, 1, 64, 64, "int8", [64], dev)
     q, lens, k = rows(1, 1, 1, 64, 3), ints(64), rows(1, 1, 1, 64, 4)
     for bad in (dict(k_scale=None), dict(v_scale=ks.double()), dict(workspace=torch.empty(1, device=dev).expand(1 << 30)),
-                dict(workspace=torch.empty(8, device=dev)), dict(prefix_k=k[0]), dict(scale=-1.0), dict(lse=ks),
+                dict(prefix_k=k[0], prefix_v=k[0], workspace=torch.empty(8, device=dev)), dict(prefix_k=k[0]), dict(scale=-1.0), dict(lse=ks),
                 dict(out=q.transpose(0, 1)[:, :, :, :32]), dict(prefix_k=k[0], prefix_v=k[0, :, :, :32])):
         with pytest.raises((TypeError, ValueError, A.FAError)):
             cache.decode_cache(q, kc, vc, lens, **{**dict(k_scale=ks, v_scale=vs), **bad})

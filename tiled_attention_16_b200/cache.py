@@ -165,14 +165,13 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, n: int | None = Non
 
 @functools.lru_cache(maxsize=1024)
 def _decode_shape(index, *fields):
-    """The C shape and its workspace (at least 256 bytes, so that what is
-    wrong with a refused shape is the library's to report)."""
+    """The C shape and its workspace on device `index`."""
     shp = FaCacheDecodeShape(*fields)
-    return shp, max(int(_cache_lib().fa_decode_cache_workspace_bytes(ctypes.byref(shp))), 256)
+    return shp, int(_cache_lib().fa_decode_cache_workspace_bytes(ctypes.byref(shp)))
 
 
 def decode_cache_workspace_bytes(B, Hq, Hkv, Nq, capacity, D, dtype=torch.bfloat16, n_prefix=0) -> int:
-    """Bytes of decode_cache's workspace on the current device."""
+    """Bytes of decode_cache's workspace on the current device (0: none needed)."""
     shp = FaCacheDecodeShape(int(B), int(Hq), int(Hkv), int(Nq), int(capacity), int(n_prefix), int(D), FORMATS[dtype],
                              1.0, 1)
     return int(_cache_lib().fa_decode_cache_workspace_bytes(ctypes.byref(shp)))
@@ -224,15 +223,19 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
         want(lse, "lse", (B, Hq, Nq), torch.float32, k_cache)
     shp, nbytes = _decode_shape(index, B, Hq, Hkv, Nq, cap, n_prefix, D, fmt,
                                 1.0 / math.sqrt(D) if scale is None else float(scale), 1 if causal else 0)
+    ws = None
     if workspace is None:
-        workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            ws = workspace.data_ptr()
     else:
         if workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous buffer on {q.device}")
         nbytes = workspace.numel() * workspace.element_size()
+        ws = workspace.data_ptr()
     st = _cache_lib().fa_decode_cache(ctypes.byref(shp), q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), ks, vs,
-                                      lens.data_ptr(), pk, pv, out.data_ptr(), lse.data_ptr(), workspace.data_ptr(),
-                                      nbytes, raw_stream(index))
+                                      lens.data_ptr(), pk, pv, out.data_ptr(), lse.data_ptr(), ws, nbytes,
+                                      raw_stream(index))
     if st != FA_OK:
         raise FAError(st, "fa_decode_cache")
     return out, lse

@@ -130,7 +130,7 @@ fa_status check_decode(const fa_cache_decode_shape* s) {
 // of e4m3 slots, device time undivided and divided: 256 slots 6.0, 6.1, 10.9 us
 // and 8.0, 9.4, 13.9; 512 slots 7.9, 7.9, 14.9 and 8.3, 10.2, 17.0; 1024 slots
 // 11.7, 11.8, 21.5 and 9.2, 10.6, 22.3.
-constexpr int kUndividedSlots = 512;
+constexpr int kUndividedSlots = FA_CACHE_UNDIVIDED;
 
 // How a decode call is split.  The cache part runs on as many CTAs as fit on
 // the SMs at once; shapes do not change that, the kernel deals its tiles out
@@ -177,10 +177,13 @@ DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
         at += up256(bytes);
         return o;
     };
-    const size_t slots = pl.undivided ? 0 : 2 * static_cast<size_t>(pl.n_cta) * pl.rows_cta;
-    pl.o_part = take(slots * s.D * 4);
-    pl.lse_part = take(slots * 4);
-    pl.meta = take(static_cast<size_t>(units) * pl.RB * 8);
+    if (!pl.undivided) {
+        const size_t slots = 2 * static_cast<size_t>(pl.n_cta) * pl.rows_cta;
+        pl.o_part = take(slots * s.D * 4);
+        pl.lse_part = take(slots * 4);
+    }
+    // (undivided units without a prefix need no join, and so no workspace)
+    if (!pl.undivided || s.n_prefix > 0) pl.meta = take(static_cast<size_t>(units) * pl.RB * 8);
     if (s.n_prefix > 0) {
         pl.o_unit = take(static_cast<size_t>(rows) * s.D * 4);
         pl.lse_unit = take(static_cast<size_t>(rows) * 4);
@@ -312,7 +315,8 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
     if (!aligned16(q) || !aligned16(o) || !aligned4(lse) || !aligned4(lens)) return FA_ERR_INVALID_ARG;
     if (!cache_pointers_ok(s.format, k_cache, v_cache, k_scale, v_scale)) return FA_ERR_INVALID_ARG;
     if (s.n_prefix > 0 && (!aligned16(k_prefix) || !aligned16(v_prefix))) return FA_ERR_INVALID_ARG;
-    if (!aligned256(workspace)) return FA_ERR_INVALID_ARG;
+    const bool no_workspace = s.capacity <= kUndividedSlots && s.n_prefix == 0;
+    if (!no_workspace && !aligned256(workspace)) return FA_ERR_INVALID_ARG;
     if ((st = static_cast<fa_status>(device_status_code())) != FA_OK) return st;
     const int sms = sm_count();
     if (sms <= 0) return FA_ERR_CUDA;
@@ -336,7 +340,7 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
     p.lse_part = f32(pl.lse_part);
     p.o_unit = s.n_prefix > 0 ? f32(pl.o_unit) : nullptr;
     p.lse_unit = s.n_prefix > 0 ? f32(pl.lse_unit) : nullptr;
-    p.meta = reinterpret_cast<int2*>(ws + pl.meta);
+    p.meta = no_workspace ? nullptr : reinterpret_cast<int2*>(ws + pl.meta);
     p.B = s.B;
     p.Hkv = s.Hkv;
     p.G = s.Hq / s.Hkv;

@@ -2,11 +2,14 @@
 // at 16 or 8 bits, and the merge with a shared prefix (include/fa_cache.h).
 //
 // Bound by HBM: each cached row is read once for the Hq / Hkv * Nq query rows
-// of its K/V head.  The lengths are in device memory, so the split is made
-// there too: all (sequence, K/V head, row block) units' 64-key tiles are laid
-// end to end and every resident CTA takes an equal run of them, whatever the
-// lengths; a run may begin and end inside a unit.  A CTA reads the lengths
-// (one warp's scan) to find its run.
+// of its K/V head (8 sequences of 32K slots, 64 query over 8 K/V heads of 128:
+// e4m3 88 us, 6.1 TB/s; int8 89; bf16 160, 6.7).  The lengths are in device
+// memory, so the split is made there too: all (sequence, K/V head) units'
+// 64-key tiles are laid end to end and every resident CTA takes an equal run of
+// them, whatever the lengths; a run may begin and end inside a unit.  A CTA
+// reads the lengths (one warp's scan) to find its run.  Many short sequences
+// are bound by what a unit costs besides its tiles (48 of up to 8100 int8
+// slots, 12 query rows: 50 us, 4.3 TB/s).
 //
 //   warp 4      producer: K and V tiles (TMA) and their scales (bulk copies)
 //               through a ring that keeps running across units
@@ -714,7 +717,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         // a part that begins before this CTA goes to its slot 2 c, one that ends after it to 2 c + 1
         const bool whole = w.t0 == 0 && w.t1 == w.tiles;
         const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
-        if (w.t0 == 0 && threadIdx.x == 0) {
+        if (w.t0 == 0 && threadIdx.x == 0 && p.meta != nullptr) {
             const long long end = w.at + p.unit_cost + w.tiles;                      // past the last tile
             const int last = static_cast<int>((end * w.n - 1) / w.total);            // its run
             p.meta[(w.b * p.Hkv + w.h) * p.RB + rb] = make_int2(whole ? -1 : slot, whole ? 1 : last - run + 1);

@@ -252,6 +252,7 @@ struct CacheDecodeParams {
     float *o_unit, *lse_unit;  // [B*Hq*Nq, D], [B*Hq*Nq]: undivided units' results for the merge with the
                                // prefix (null without one: they go to o and lse)
     int2* meta;              // [B * Hkv * RB]: a unit's first slot (-1: undivided) and parts, for each row block
+                             // (null: no join follows)
     int B, Hkv, G, Nq, capacity, causal;
     int rows_cta, RB;        // query rows a CTA holds (8 or 16), row blocks of a K/V head
     int n_cta;
