@@ -236,3 +236,47 @@ def test_decode_definition_agrees_with_the_attention_oracle():
     o, lse = oracle.attention_forward_kv(q, k, v, 0.2, True)
     a = so.decode_cache(q, k[:, :, 12:], v[:, :, 12:], [8, 8], 0.2, True, k[0, :, :12], v[0, :, :12])
     assert np.allclose(a[0], o) and np.allclose(a[1], lse)
+
+
+# ---- the headers from plain C
+
+C_CHECK = r"""
+#include <stdint.h>
+#include <stdio.h>
+#include "fa_cache.h"
+#define CHECK(n, cond) do { if (!(cond)) { fprintf(stderr, "check %d: %s\n", n, #cond); return n; } } while (0)
+int main(void) {
+    void* p = (void*)(uintptr_t)0x10000;   /* never dereferenced */
+    fa_rows rows = {0, 4096, 128, 512};
+    fa_rope_shape rs = {1, 4, 2, 8, 96, 0, 0, 1e-6f, 0};
+    fa_cache_shape cs = {1, 2, 10, 128, FA_CACHE_INT8};
+    fa_cache_decode_shape ds = {1, 4, 2, 1, 12, 0, 128, FA_CACHE_E4M3, 0.0f, 1};
+    rows.data = p;
+    CHECK(1, fa_qk_norm_rope(&rs, &rows, &rows, p, p, 0, 0, p, p, 0) == FA_ERR_UNSUPPORTED);
+    CHECK(2, fa_qk_norm_rope_bwd_workspace_bytes(&rs) == 0);
+    CHECK(3, fa_qk_norm_rope_bwd(&rs, p, p, &rows, &rows, p, p, 0, 0, &rows, &rows, p, p, p, 0, 0) == FA_ERR_UNSUPPORTED);
+    CHECK(4, fa_cache_write(&cs, 1, &rows, &rows, p, 0, p, p, p, p, 0) == FA_ERR_INVALID_ARG);
+    CHECK(5, fa_cache_read(&cs, 1, 0, p, p, p, p, p, p, 0) == FA_ERR_INVALID_ARG);
+    CHECK(6, fa_decode_cache_workspace_bytes(&ds) == 0);
+    CHECK(7, fa_decode_cache(&ds, p, p, p, p, p, p, 0, 0, p, p, p, 0, 0) == FA_ERR_INVALID_ARG);
+    CHECK(8, FA_CACHE_BF16 == 0 && FA_CACHE_UNDIVIDED == 512);
+    printf("ok\n");
+    return 0;
+}
+"""
+
+
+def test_headers_compile_as_c99(tmp_path):
+    import os
+    import shutil
+    import subprocess
+    from tiled_attention_16_b200.build import LIB, ROOT
+    if shutil.which("gcc") is None:
+        pytest.skip("gcc not available")
+    src, exe = tmp_path / "check.c", tmp_path / "check"
+    src.write_text(C_CHECK)
+    r = subprocess.run(["gcc", "-std=c99", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(ROOT, "include"), str(src), LIB,
+                        f"-Wl,-rpath,{os.path.dirname(LIB)}", "-o", str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stderr
+    r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
+    assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
