@@ -9,8 +9,8 @@
  *   FA_CACHE_BF16  bf16 values
  *   FA_CACHE_E4M3  1-byte e4m3 codes (OCP FP8 E4M3) with one fp32 scale a row
  *   FA_CACHE_INT8  1-byte signed codes with one fp32 scale a row
- * k_scale, v_scale fp32 [B, Hkv, capacity] (NULL for bf16): a code stands for
- * code * scale.  The writer's rules, for a row with largest magnitude amax:
+ * k_scale, v_scale fp32 [B, Hkv, capacity] (NULL for bf16), >= 0 or NaN: a code
+ * stands for code * scale.  The writer's rules, for a row with largest magnitude amax:
  *   e4m3  scale = 2^e with the smallest e >= -120 such that amax <= 448 * 2^e
  *         (dividing by it is exact, so a value is rounded once, to the nearest
  *         code, ties to even; a scale that is no power of two would gain no
@@ -87,7 +87,10 @@ FA_API size_t fa_decode_cache_workspace_bytes(const fa_cache_decode_shape* shape
  * when n_prefix is 0).  o [B,Hq,Nq,D] bf16, lse [B,Hq,Nq] fp32 (natural log).
  * The prefix is read once for the whole batch: its rows of all sequences meet
  * it as one matrix.  The 8-bit formats multiply in fp16 on the codes (exact
- * there), q scaled by a power of two for each row; scales enter in fp32.
+ * there), q scaled by a power of two for each row; scales enter in fp32.  P
+ * times the V scales is rounded to fp16 (2^-11 of each weight, and for weights
+ * far below the largest up to 2^-30 of the sequence's largest V value); with
+ * bf16 caches and prefixes P is rounded to bf16 (2^-8).
  * workspace: 256-byte aligned (NULL allowed where 0 bytes are needed), contents
  * on entry do not matter; calls that may overlap need workspaces of their own.
  * Codes below a sequence's length

@@ -7,6 +7,10 @@ fp16 (2^-11), so O moves by at most that times sum_j p_j |v_j|; a score is a
 sum of D products in fp32, off by at most (D + 16) 2^-23 of its largest sum of
 magnitudes, which moves every weight by that (twice: numerator and sum); the
 exponentials and the fp32 sums add 2^-18; the result is rounded to bf16 (2^-8).
+8-bit caches: a weight times its V scale, the row's largest weight at 2^6 or more
+and the scale over a power of two below twice the largest, is subnormal in fp16
+below 2^-14 and then off by up to 2^-25, so each key may add 2^-25 / 2^6 * 2 =
+2^-30 of the largest |scale * code| there is.
 """
 import numpy as np
 import pytest
@@ -191,6 +195,11 @@ def test_captured_write_follows_the_device_lengths():
 
 # ---------------------------------------------------------------- decoding
 
+def lens_mask(lens, shape):
+    """Which of [B, H, cap, D] lie below the lengths."""
+    return np.broadcast_to((np.arange(shape[2]) < lens.cpu().numpy()[:, None])[:, None, :, None], shape)
+
+
 def check_decode(q, kc, vc, ks, vs, lens, got, causal=True, scale=None, pk=None, pv=None):
     D = q.shape[-1]
     scale = D ** -0.5 if scale is None else scale
@@ -206,6 +215,9 @@ def check_decode(q, kc, vc, ks, vs, lens, got, causal=True, scale=None, pk=None,
     assert (np.isneginf(gl) == np.isneginf(lse)).all() and (go[np.isneginf(lse)] == 0).all()
     some = ~np.isneginf(lse)
     tol = (u * 1.01 + 2 * ds + 2.0 ** -18)[..., None] * wt + BF * 1.01 * np.abs(o)
+    if ks is not None:
+        top = np.repeat(np.abs(values(vc, vs)).max((2, 3), initial=0.0, where=lens_mask(lens, v.shape)), q.shape[1] // v.shape[1], 1)
+        tol = tol + (2.0 ** -30 * top * np.clip(lens.cpu().numpy(), 0, v.shape[2])[:, None])[..., None, None]
     err = np.abs(go - o)
     assert (err[some] <= tol[some]).all(), f"O off by {(err[some] / tol[some]).max()} of its tolerance"
     tl = ds + 2.0 ** -18 + 2.0 ** -22 * np.abs(np.where(some, lse, 0))
