@@ -229,7 +229,7 @@ struct CacheWriteParams {
     void *k_cache, *v_cache;
     float *k_scale, *v_scale;
     int B, H, N, capacity;
-    int k_shift, v_shift;    // filled by the launch
+    int shift;               // log2 of a tile's heads; filled by the launch
 };
 struct CacheReadParams {
     const void *k_cache, *v_cache;
