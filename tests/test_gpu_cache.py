@@ -327,6 +327,57 @@ def test_poisoned_rows_reach_the_queries_that_see_them_only(fmt):
     assert torch.isnan(o[2]).all() and torch.isnan(lse[2]).all()
 
 
+# hidden(j): keys whose score is -inf, of each sequence's own and of the prefix
+MINUS_INF = [
+    # B, Hq, Hkv, Nq, cap, D, Np, own, prefix
+    (3, 8, 2, 1, 700, 128, 0, lambda j: j < 100, None),        # whole first tiles, a second row without them
+    (3, 4, 4, 2, 300, 64, 0, lambda j: j % 3 != 1, None),
+    (2, 4, 1, 1, 132, 128, 0, lambda j: j >= 0, None),         # every key
+    (3, 4, 2, 1, 64, 64, 900, lambda j: j < 0, lambda j: j >= 0),              # the whole prefix, alternating blocks
+    (3, 4, 2, 1, 64, 128, 900, lambda j: j < 20, lambda j: j // 128 % 2 == 0),   # one block's tiles of it
+    (40, 8, 2, 1, 4, 128, 700, lambda j: j < 1, lambda j: j < 500),            # row tiles that share the keys
+    (40, 8, 2, 1, 4, 64, 200, lambda j: j >= 0, lambda j: j >= 0),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,cap,D,Np,own,prefix", MINUS_INF)
+def test_scores_of_minus_infinity_are_hidden_keys(B, Hq, Hkv, Nq, cap, D, Np, own, prefix):
+    """As in fa_decode.  The queries' first value is positive, and -inf in the
+    keys' first place makes their scores -inf."""
+    dev = _gpu()
+    lens = [cap - (b % 3) for b in range(B)]
+    kc, vc, _, _ = filled(B, Hkv, cap, D, "bf16", lens, dev)
+    q = rows(B, Hq, Nq, D, 78)
+    q[..., 0] = q[..., 0].abs() + 0.5
+    mine = np.array([bool(own(j)) for j in range(cap)])
+    kc[:, :, torch.from_numpy(mine).to(dev), 0] = float("-inf")
+    pk = pv = None
+    shared = np.zeros(0, dtype=bool)
+    if Np:
+        pk, pv = rows(1, Hkv, Np, D, 3)[0].contiguous(), rows(1, Hkv, Np, D, 4)[0].contiguous()
+        shared = np.array([bool(prefix(j)) for j in range(Np)])
+        pk[:, torch.from_numpy(shared).to(dev), 0] = float("-inf")
+    o, lse = cache.decode_cache(q, kc, vc, ints(*lens), prefix_k=pk, prefix_v=pv)
+    assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
+    go, gl, qq, k, v = np64(o), np64(lse), np64(q), np64(kc), np64(vc)
+    fk, fv = (np.zeros((Hkv, 0, D)),) * 2 if pk is None else (np64(pk), np64(pv))
+    for b in range(B):
+        for h in range(Hq):
+            g = h // (Hq // Hkv)
+            for i in range(Nq):
+                n = lens[b] - Nq + i + 1
+                keep = np.concatenate([~shared, ~mine[:n]])
+                ro, rl, wt, size = so.decode_rows(qq[b, h, i], np.concatenate([fk[g], k[b, g, :n]]),
+                                                  np.concatenate([fv[g], v[b, g, :n]]), D ** -0.5, keep)
+                if not keep.any():
+                    assert np.isneginf(gl[b, h, i]) and (go[b, h, i] == 0).all()
+                    continue
+                ds = (D + 16) * 2.0 ** -23 * size
+                tol = (BF * 1.01 + 2 * ds + 2.0 ** -18) * wt + BF * 1.01 * np.abs(ro)
+                assert (np.abs(go[b, h, i] - ro) <= tol).all()
+                assert abs(gl[b, h, i] - rl) <= ds + 2.0 ** -18 + 2.0 ** -22 * abs(rl)
+
+
 @pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
 def test_lengths_out_of_range_are_clamped(fmt):
     dev = _gpu()

@@ -38,6 +38,8 @@
 #include "fa_internal.h"
 #include "sm100.cuh"
 
+#include <cfloat>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -366,6 +368,9 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     constexpr int kStages = L::kStages;
     constexpr int kSteps = D / 16;
     constexpr float kShift = kHalf ? 6.f : 0.f;   // P is 2^kShift where the score is the row's (stale) maximum
+    // Stands for kShift less the maximum of a row that has none yet: any finite
+    // score plus it asks for a maximum, and -inf (a hidden key) stays -inf, no NaN.
+    constexpr float kFar = FLT_MAX;
     extern __shared__ __align__(1024) uint8_t smem[];   // the swizzle's alignment
     uint64_t* full = reinterpret_cast<uint64_t*>(smem + L::kBar);
     uint64_t* empty = full + kStages;
@@ -500,7 +505,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         if (p.causal) pos_min = w.len - p.Nq;
 
         float o[NT][kSteps][4];
-        // stale row maximum, kShift less it (infinite before the first key), partial row sum
+        // stale row maximum, kShift less it (kFar before the first key), partial row sum
         float m_run[NT][2], nm[NT][2], l_run[NT][2];
         float v_top = __int_as_float(1 << 23);   // power of two that bounds the V scales so far
         float v_inv = pow2_inverse(v_top);
@@ -509,7 +514,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
             for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
             m_run[n][0] = m_run[n][1] = -INFINITY;
-            nm[n][0] = nm[n][1] = INFINITY;
+            nm[n][0] = nm[n][1] = kFar;
             l_run[n][0] = l_run[n][1] = 0.f;
         }
 
@@ -611,12 +616,11 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                         const float m_new = fmaxf(m_run[n][h], mx);
                         alpha[h] = m_new == -INFINITY ? 1.f : ex2(m_run[n][h] - m_new);
                         m_run[n][h] = m_new;
-                        nm[n][h] = kShift - m_new;
+                        nm[n][h] = m_new == -INFINITY ? kFar : kShift - m_new;
                         l_run[n][h] *= alpha[h];
                         alpha[h] *= vfac;
-                        // -inf + inf is NaN where a row has seen no key yet
-                        y[n][h] = kEdge && xa == -INFINITY ? xa : xa + nm[n][h];
-                        y[n][2 + h] = kEdge && xb == -INFINITY ? xb : xb + nm[n][h];
+                        y[n][h] = xa + nm[n][h];
+                        y[n][2 + h] = xb + nm[n][h];
                     }
 #pragma unroll
                     for (int j = 0; j < kSteps; ++j) {

@@ -389,7 +389,9 @@ fa_prefix_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant_
                     if (!__all_sync(0xffffffffu, ok)) { ok = false; break; }
                     const float2 o1 = *ml;
                     const float M = join ? fmaxf(m_used, o1.x) : m_used;
-                    const float w0 = ex2(m_used - M), w1 = join ? ex2(o1.x - M) : 0.f;   // NaN stays NaN
+                    // no key in either block (all scores -inf): weights and sum 0; NaN stays NaN
+                    const bool none = M == -INFINITY;
+                    const float w0 = none ? 0.f : ex2(m_used - M), w1 = none || !join ? 0.f : ex2(o1.x - M);
                     const float ls = join ? w0 * l + w1 * o1.y : l;
                     f0 = w0 / ls;
                     f1 = w1 / ls;
