@@ -57,10 +57,10 @@ typedef struct {
 } fa_rope_shape;
 
 /* q [B,Hq,N,D], k [B,Hkv,N,D] bf16 views; q_weight, k_weight [D];
- * inv_freq fp32 [rotary_dim / 2] (NULL allowed when rotary_dim is 0);
+ * inv_freq fp32 [rotary_dim / 2], finite (NULL allowed when rotary_dim is 0);
  * positions int32 [B,N], or NULL: token n of each sequence is at position n.
- * q_out [B,Hq,N,D], k_out [B,Hkv,N,D] bf16 contiguous.  Outputs 16-byte
- * aligned, weights, inv_freq and positions 4-byte. */
+ * q_out [B,Hq,N,D], k_out [B,Hkv,N,D] bf16 contiguous, apart from the inputs.
+ * Outputs 16-byte aligned, weights, inv_freq and positions 4-byte. */
 FA_API fa_status fa_qk_norm_rope(const fa_rope_shape* shape, const fa_rows* q, const fa_rows* k, const void* q_weight,
                                  const void* k_weight, const float* inv_freq, const int* positions, void* q_out,
                                  void* k_out, void* stream);
