@@ -512,6 +512,22 @@ def test_refusals_on_the_gpu():
     assert A.device_status(dev) == A.FA_OK
 
 
+def test_refusals_of_what_is_no_tensor_and_of_too_many_rows():
+    dev = _gpu()
+    kc, vc, ks, vs = filled(1, 1, 64, 64, "int8", [64], dev)
+    q, lens, k = rows(1, 1, 1, 64, 3), ints(64), rows(1, 1, 1, 64, 4)
+    for args, more in (((None, kc, vc, lens), {}), ((q, None, vc, lens), {}), ((q, kc, None, lens), {}),
+                       ((q, kc, vc, None), {}), ((q, kc, vc, [64]), {}), ((q, kc, vc, lens), dict(workspace=7)),
+                       ((q, kc, vc, lens), dict(prefix_k=[1], prefix_v=[1]))):
+        with pytest.raises((TypeError, ValueError)):
+            cache.decode_cache(*args, **{**dict(k_scale=ks, v_scale=vs), **more})
+    many = k.expand(1, 1, 2 ** 32 + 1, 64)       # wraps to one row in 32 bits
+    for args in ((None, k, kc, vc, lens), (k, None, kc, vc, lens), (many, many, kc, vc, lens)):
+        with pytest.raises((TypeError, ValueError)):
+            cache.cache_write(*args, k_scale=ks, v_scale=vs)
+    assert A.device_status(dev) == A.FA_OK
+
+
 def test_bf16_cache_agrees_with_decode():
     """Full lengths: the same attention as decode over the same history."""
     dev = _gpu()

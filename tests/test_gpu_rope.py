@@ -206,6 +206,18 @@ def test_refusals_on_the_gpu():
     assert A.device_status(q.device) == A.FA_OK
 
 
+def test_refusals_of_what_is_no_tensor():
+    q, k, qw, kw, inv, pos, dq, dk = make(1, 2, 1, 4, 64, 64, seed=2)
+    for args in ((None, k, qw, kw, inv), (q, None, qw, kw, inv), (q, k, None, kw, inv), (q, k, qw, None, inv),
+                 (q, k, qw, kw, [1.0]), (q, k, qw, kw, inv, [0, 1, 2, 3])):
+        with pytest.raises((TypeError, ValueError)):
+            rope.qk_norm_rope(*args)
+    for args, more in (((None, dk), {}), ((dq, None), {}), ((dq, dk), dict(workspace=7)), ((dq, dk), dict(dq=3))):
+        with pytest.raises((TypeError, ValueError)):
+            rope.qk_norm_rope_bwd(*args, q, k, qw, kw, inv, **more)
+    assert A.device_status(q.device) == A.FA_OK
+
+
 def test_broadcast_inputs():
     """Views whose rows repeat (stride 0) are read like any other."""
     q, k, qw, kw, inv, pos, dq, dk = make(2, 4, 2, 9, 128, 64, seed=4)

@@ -107,9 +107,11 @@ def cache_write(k: torch.Tensor, v: torch.Tensor, k_cache: torch.Tensor, v_cache
     outside the cache are dropped; all other slots stay as they are."""
     fmt, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
     B, Hkv, cap, D = k_cache.shape
-    if k.dim() != 4:
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
         raise ValueError("k must be [B, Hkv, N, D]")
     N = k.shape[2]
+    if N > 0x7FFFFFFF:       # (a broadcast view; more than the C side's int holds)
+        raise ValueError(f"k has {N} rows a head, more than 2^31 - 1")
     shape = (B, Hkv, N, D)
     kr, vr = check_rows(k, "k", shape, k_cache), check_rows(v, "v", shape, k_cache)
     want(start, "start", (B,), torch.int32, k_cache)
@@ -188,7 +190,7 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     share and which is read once for the batch.  Query i stands at slot
     lens[b] - Nq + i.  Returns (o [B,Hq,Nq,D] bf16, lse [B,Hq,Nq] fp32); a
     query that sees no key gets 0 and -inf."""
-    if q.dim() != 4:
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
         raise ValueError("q must be [B, Hq, Nq, D]")
     fmt, ks, vs = _check_cache(k_cache, v_cache, k_scale, v_scale)
     _, Hkv, cap, D = k_cache.shape
@@ -201,7 +203,7 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
     if prefix_k is not None or prefix_v is not None:
         if prefix_k is None or prefix_v is None:
             raise ValueError("prefix_k and prefix_v come together")
-        if prefix_k.dim() != 3:
+        if not isinstance(prefix_k, torch.Tensor) or prefix_k.dim() != 3:
             raise ValueError("prefix_k must be [Hkv, Np, D]")
         n_prefix = prefix_k.shape[1]
         want(prefix_k, "prefix_k", (Hkv, n_prefix, D), torch.bfloat16, k_cache)
@@ -229,7 +231,7 @@ def decode_cache(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, 
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
             ws = workspace.data_ptr()
     else:
-        if workspace.get_device() != index or not workspace.is_contiguous():
+        if not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
             raise ValueError(f"workspace must be a contiguous buffer on {q.device}")
         nbytes = workspace.numel() * workspace.element_size()
         ws = workspace.data_ptr()

@@ -78,18 +78,20 @@ def check_rows(t: torch.Tensor, name: str, shape, first: torch.Tensor | None = N
 
 
 def _common(q, k, q_weight, k_weight, inv_freq, positions, eps, interleaved):
-    if q.dim() != 4 or k.dim() != 4:
+    if not isinstance(q, torch.Tensor) or not isinstance(k, torch.Tensor) or q.dim() != 4 or k.dim() != 4:
         raise ValueError("q and k must be [B, H, N, D]")
     B, Hq, N, D = q.shape
     Hkv = k.shape[1]
     qr, kr = check_rows(q, "q", (B, Hq, N, D)), check_rows(k, "k", (B, Hkv, N, D), q)
-    wt = q_weight.dtype
+    wt = getattr(q_weight, "dtype", None)
     if wt != torch.float32 and wt != torch.bfloat16:
         raise TypeError(f"q_weight must be torch.bfloat16 or torch.float32, got {wt}")
     want(q_weight, "q_weight", (D,), wt, q)
     want(k_weight, "k_weight", (D,), wt, q)
     rot = 0
     if inv_freq is not None:
+        if not isinstance(inv_freq, torch.Tensor):
+            raise TypeError("inv_freq must be a torch.Tensor")
         rot = 2 * inv_freq.numel()
         want(inv_freq, "inv_freq", (rot // 2,), torch.float32, q)
     if positions is not None:
@@ -159,7 +161,7 @@ def qk_norm_rope_bwd(dq_out: torch.Tensor, dk_out: torch.Tensor, q: torch.Tensor
     dkw = torch.empty(D, dtype=torch.float32, device=dev)
     if workspace is None:
         workspace = torch.empty(_bwd_workspace(D, index), dtype=torch.uint8, device=dev)
-    elif workspace.get_device() != index or not workspace.is_contiguous():
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != index or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous buffer on {q.device}")
     st = L.fa_qk_norm_rope_bwd(ctypes.byref(shp), dq_out.data_ptr(), dk_out.data_ptr(), ctypes.byref(qr),
                                ctypes.byref(kr), qw, kw, freq, pos, ctypes.byref(dqr), ctypes.byref(dkr),
