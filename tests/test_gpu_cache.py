@@ -327,6 +327,25 @@ def test_poisoned_rows_reach_the_queries_that_see_them_only(fmt):
     assert torch.isnan(o[2]).all() and torch.isnan(lse[2]).all()
 
 
+ROWS = [
+    # B, Hq, Hkv, Nq, cap, D, lens, causal: query rows a K/V head from 9 to 100, around what a CTA holds
+    (3, 9, 1, 1, 300, 128, [300, 1, 77], True),
+    (2, 34, 2, 1, 1100, 64, [1100, 513], True),
+    (2, 10, 1, 2, 1028, 128, [1, 1027], True),
+    (5, 32, 1, 1, 2000, 128, [2000, 64, 65, 0, 1999], True),
+    (3, 16, 2, 4, 700, 64, [700, 3, 64], True),
+    (2, 33, 1, 1, 516, 128, [515, 100], False),
+    (2, 20, 1, 5, 900, 64, [4, 899], True),
+    (48, 8, 2, 8, 200, 128, [(11 * b) % 201 for b in range(48)], True),
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,cap,D,lens,causal", ROWS)
+def test_decode_many_rows_a_head(fmt, B, Hq, Hkv, Nq, cap, D, lens, causal):
+    test_decode_ragged(fmt, B, Hq, Hkv, Nq, cap, D, lens, causal)
+
+
 # hidden(j): keys whose score is -inf, of each sequence's own and of the prefix
 MINUS_INF = [
     # B, Hq, Hkv, Nq, cap, D, Np, own, prefix

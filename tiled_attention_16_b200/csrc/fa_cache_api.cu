@@ -126,10 +126,10 @@ fa_status check_decode(const fa_cache_decode_shape* s) {
 }
 
 // Capacity up to which a (sequence, K/V head) is one CTA's: no join is needed
-// then, which saves a launch.  Measured with 8 K/V heads and 1, 8, 64 sequences
-// of e4m3 slots, device time undivided and divided: 256 slots 6.0, 6.1, 10.9 us
-// and 8.0, 9.4, 13.9; 512 slots 7.9, 7.9, 14.9 and 8.3, 10.2, 17.0; 1024 slots
-// 11.7, 11.8, 21.5 and 9.2, 10.6, 22.3.
+// then, which saves a launch.  Measured with 32 query over 8 K/V heads and 1, 8,
+// 64 sequences of e4m3 slots, device time undivided and divided: 256 slots 6.0,
+// 6.1, 13.9 us and 8.3, 9.1, 15.0; 512 slots 8.1, 8.2, 21.7 and 8.5, 10.0, 20.5;
+// 1024 slots 12.1, 12.2, 35.6 and 9.1, 10.7, 31.5.
 constexpr int kUndividedSlots = FA_CACHE_UNDIVIDED;
 
 // How a decode call is split.  The cache part runs on as many CTAs as fit on
@@ -145,12 +145,14 @@ struct DecodeCachePlan {
 DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
     DecodeCachePlan pl{};
     const int R = s.Hq / s.Hkv * s.Nq;
-    pl.rows_cta = R <= 8 ? 8 : 16;
+    // 8 sequences of 32K slots of 8 heads of 128, with 32 rows a CTA and with twice
+    // 16: 24 int8 rows 142 and 170 us, 32 rows e4m3 153 and 150, bf16 168 and 188.
+    pl.rows_cta = R <= 8 ? 8 : R <= 16 ? 16 : 32;
     pl.RB = (R + pl.rows_cta - 1) / pl.rows_cta;
     // runs of tiles, and RB CTAs to each
     const long long units = static_cast<long long>(s.B) * s.Hkv;
     const long long most = units * ((s.capacity + 63LL) / 64);
-    const long long resident = static_cast<long long>(sms) * cache_decode_ctas_per_sm(s.D, s.format);
+    const long long resident = static_cast<long long>(sms) * cache_decode_ctas_per_sm(s.D, s.format, pl.rows_cta);
     pl.undivided = s.capacity <= kUndividedSlots;
     pl.n_cta = static_cast<int>(pl.undivided ? units : std::max(1LL, std::min(most, resident / pl.RB))) * pl.RB;
     const long long rows = static_cast<long long>(s.B) * s.Hq * s.Nq;

@@ -3,22 +3,27 @@
 //
 // Bound by HBM: each cached row is read once for the Hq / Hkv * Nq query rows
 // of its K/V head (8 sequences of 32K slots, 64 query over 8 K/V heads of 128:
-// e4m3 88 us, 6.1 TB/s; int8 89; bf16 160, 6.7).  The lengths are in device
+// e4m3 88 us, 6.1 TB/s; int8 88; bf16 157, 6.8).  The lengths are in device
 // memory, so the split is made there too: all (sequence, K/V head) units'
 // 64-key tiles are laid end to end and every resident CTA takes an equal run of
 // them, whatever the lengths; a run may begin and end inside a unit.  A CTA
 // reads the lengths (one warp's scan) to find its run.  Many short sequences
 // are bound by what a unit costs besides its tiles (48 of up to 8100 int8
-// slots, 12 query rows: 50 us, 4.3 TB/s).
+// slots, 12 query rows: 46 us, 4.6 TB/s).
 //
 //   warp 4      producer: K and V tiles (TMA) and their scales (bulk copies)
 //               through a ring that keeps running across units
-//   warps 0-3   16 keys of every tile each, with the keys as the M axis of
-//               warp-level m16n8k16 MMAs:
-//                 S^T [16 keys, rows]  = K [16, D] Q^T
-//                 O^T [D, rows]       += V^T [D, 16] P^T
-//               so that 8 query rows (one K/V head's group, usually) fill the
-//               N axis; P^T is turned by movmatrix between the two.
+//   warps 0-3   warp-level m16n8k16 MMAs with keys, then columns, as the M axis,
+//               so that 8 query rows (one K/V head's group, usually) fill the N
+//               axis.  A warp takes 16 keys of every tile for the scores and a
+//               quarter of the columns for the output:
+//                 S^T [16 keys, rows]    = K [16, D] Q^T
+//                 O^T [D / 4, rows]     += V^T [D / 4, 64 keys] P^T
+//               P^T is turned by movmatrix and handed round in shared memory
+//               (two buffers, so one barrier a tile).  A warp that kept its keys
+//               for both products would need no barrier, but all D columns of
+//               O: then a unit's end joins four accumulators (51 us instead of
+//               46 in the case above) and 32 rows do not fit a CTA.
 // 8-bit codes are exact in fp16 and so are the products' operands: q is scaled
 // by a power of two for each row (its largest value in [2^14, 2^15), values
 // below 2^-29 of that lose bits), the K scale multiplies S in fp32, and the V
@@ -29,7 +34,8 @@
 // before that.  With bf16 caches P is rounded to bf16 (2^-8).  The maximum in
 // use is replaced only when a score exceeds it by more than 8 (log2 units), and
 // the bound on the V scales when one exceeds it, so most tiles need one vote
-// and no shuffles or rescaling.
+// (which is the barrier) and no shuffles or rescaling.  All four warps use the
+// same maxima and bound.
 //
 // The order of the contraction is free, so a lane reads 16 consecutive codes
 // of a key with one shared-memory load and uses them as its four k-steps; for
@@ -60,20 +66,25 @@ struct CdLayout {
     static constexpr bool kWide = kFmt == 0 && D == 128;                // 32 KB a stage
     // CTAs an SM holds at once, by shared memory and by registers (five warps
     // of at most 128 registers three times, of 168 twice)
-    static constexpr int kCtas = kWide ? 2 : 3;
+    static constexpr int kCtas = kWide || NT == 4 ? 2 : 3;
     static constexpr int kTileBytes = kCdKeys * D * kElem;              // one K or V tile
     static constexpr int kScaleBytes = kFmt == 0 ? 0 : kCdKeys * 4;
-    static constexpr int kStages = D == 128 ? 3 : (kFmt == 0 ? 3 : 6);
     static constexpr int kQFrag = NT * (D / 16) * 32 * 8;               // Q^T fragments of a unit
+    static constexpr int kPFrag = 4 * NT * 32 * 8;                      // P^T fragments of a tile
+    // Enough bytes under way for the copy rate, and no more: HBM serves fewer at
+    // once better (8 sequences of 32K slots of 8 heads, stages: e4m3 at 128
+    // 2: 89.9 us, 3: 88.1, 4: 92.3; bf16 at 128 2: 156.5, 3: 161; 16 sequences at
+    // 64, e4m3 3: 98.0, 4: 94.5, 5: 99.2; bf16 2: 83.9, 3: 84.3, 4: 88.5).
+    static constexpr int kStages = D == 128 ? (kFmt == 0 ? 2 : 3) : kFmt == 0 ? 2 : 4;
     static constexpr int kK = 0;
     static constexpr int kV = kStages * kTileBytes;
     static constexpr int kScales = 2 * kStages * kTileBytes;            // K then V scales of each stage
     static constexpr int kQ = kScales + 2 * kStages * kScaleBytes;      // two units' fragments,
     static constexpr int kQScale = kQ + 2 * kQFrag;                     // and their rows' factors
-    static constexpr int kMerge = kQScale + 2 * NT * 8 * 4;             // [4 warps][8 rows][kCols + 4] fp32
-    static constexpr int kCols = kWide ? (NT == 1 ? 64 : 32) : D;       // a round of the join: 0.7 us
-    static constexpr int kMl = kMerge + 4 * 8 * (kCols + 4) * 4;        // m, l and V exponent of the warps
-    static constexpr int kBar = kMl + 4 * 40 * 4;
+    static constexpr int kP = kQScale + 2 * NT * 8 * 4;                 // two tiles' fragments
+    static constexpr int kMx = kP + 2 * kPFrag;                         // the warps' row maxima, V scales' maxima
+    static constexpr int kMl = kMx + 4 * NT * 8 * 4 + 16;               // and row sums
+    static constexpr int kBar = kMl + 4 * NT * 8 * 4;
     static constexpr int kAlloc = kBar + (2 * kStages + 4) * 8 + 16;
     static_assert((kAlloc + 1024) * kCtas <= 228 * 1024, "CTAs must fit");
 };
@@ -201,8 +212,8 @@ __device__ __forceinline__ int seq_tiles(const CacheDecodeParams& p, int b) {
 // tile.  All units lie end to end and run c of n takes positions
 // [total c / n, total (c + 1) / n).  With more query rows a K/V head than a CTA
 // holds, RB CTAs take a run, one a block of rows, at the same time: the tiles
-// come from HBM once and from L2 for the others (8 sequences of 32K slots, 32
-// rows a head: 163 us, 174 with the row blocks as units of their own).
+// come from HBM once and from L2 for the others (8 sequences of 32K slots, two
+// blocks of 16 rows: 163 us, 174 with the row blocks as units of their own).
 struct Walk {
     int x0, x1, total, n;       // the run's positions, all positions, runs with any
     int b, h, at, tiles, len;   // unit, its first position, its tiles, its sequence's length
@@ -283,6 +294,17 @@ __device__ __forceinline__ Walk find_run(const CacheDecodeParams& p, int c, int 
         at += __shfl_sync(0xffffffffu, incl, 31);
     }
     return w;
+}
+
+// Whether any thread of the four compute warps says so; also their barrier.
+__device__ __forceinline__ bool any_of_warps(bool x) {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred a, b;\n\t"
+                 "setp.ne.u32 a, %1, 0;\n\t"
+                 "bar.red.or.pred b, 1, 128, a;\n\t"
+                 "selp.u32 %0, 1, 0, b;\n\t}"
+                 : "=r"(r) : "r"(static_cast<uint32_t>(x)) : "memory");
+    return r != 0u;
 }
 
 __device__ __forceinline__ void cd_drain(uint64_t* bar, uint32_t parity) {
@@ -462,28 +484,35 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
     // ---------------------------------------------------------------- compute
     const int g8 = lane >> 2, t4 = lane & 3;
     const int kw = warp * 16;                       // this warp's 16 keys in a tile
+    constexpr int kBlocks = D / 64;                 // and its blocks of 16 columns of V
     const uint32_t sK = smem_u32(smem + L::kK), sV = smem_u32(smem + L::kV), sS = smem_u32(smem + L::kScales);
     const uint32_t sQ = smem_u32(smem + L::kQ), sQScale = smem_u32(smem + L::kQScale);
-    float* merge = reinterpret_cast<float*>(smem + L::kMerge);
-    float* ml = reinterpret_cast<float*>(smem + L::kMl);   // [warp]: m [16], l [16], V exponent
+    const uint32_t sP = smem_u32(smem + L::kP) + lane * 8;
+    float* mx = reinterpret_cast<float*>(smem + L::kMx);   // [warp][8 NT], then [warp]
+    float* ml = reinterpret_cast<float*>(smem + L::kMl);   // [warp][8 NT]
     const int R = p.G * p.Nq;
     // Where this lane reads in a K and in a V tile: the chunk of the first step;
-    // chunk_at() gives the others (tile bases are multiples of the swizzle).
+    // chunk_at() gives the others (tile bases are multiples of the swizzle, and
+    // so are 16 keys).
     //   8 bits  K: keys kw + g8 (+ 8), chunks 2 t4 + hh of 16 codes;
-    //           V: matrices (keys lo, hi) x (chunks j, j + 1)
+    //           V: matrices (keys lo, hi) x (chunks j, j + 1), at D = 64 (keys
+    //           lo, hi) x (this 16 keys, the next)
     //   bf16    K: matrices (keys lo, hi) x (d lo, hi);  V: (d lo, hi) x (keys lo, hi)
     const int mi = lane >> 3;
+    constexpr int kRow16 = 16 * (D * L::kElem > 128 ? 128 : D * L::kElem);   // bytes 16 keys are apart
     const uint32_t k_at = kHalf ? chunk_off<D, kFmt>(kw + g8, D == 128 ? 2 * t4 : t4)
                                 : chunk_off<D, kFmt>(kw + (mi & 1) * 8 + (lane & 7), mi >> 1);
-    const uint32_t v_at = kHalf ? chunk_off<D, kFmt>(kw + (mi & 1) * 8 + (lane & 7), mi >> 1)
-                                : chunk_off<D, kFmt>(kw + (mi >> 1) * 8 + (lane & 7), mi & 1);
+    const uint32_t v_at = !kHalf ? chunk_off<D, kFmt>((mi >> 1) * 8 + (lane & 7), 2 * kBlocks * warp + (mi & 1))
+                          : D == 128 ? chunk_off<D, kFmt>((mi & 1) * 8 + (lane & 7), 2 * warp + (mi >> 1))
+                                     : chunk_off<D, kFmt>(mi * 8 + (lane & 7), warp);
     bool ok = true;
     int unit = 0;
     int st = 0;            // ring stage and its parity
     uint32_t phase = 0u;
+    uint32_t p_buf = 0u;   // offset of the tile's P fragments
 
-    // After a wait that gave up, the remaining units are walked without loads
-    // or outputs, so that the barriers below stay matched.
+    // After a wait that gave up, the remaining tiles are worked on as they are
+    // and not written, so that the barriers stay matched.
     for (; more; w.step(p), more = w.settle(p)) {
         // ---- one unit, or the CTA's part of it
         const size_t rows_at = static_cast<size_t>(w.b * p.Hkv + w.h) * R;   // first query row of the K/V head
@@ -504,15 +533,16 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             }
         if (p.causal) pos_min = w.len - p.Nq;
 
-        float o[NT][kSteps][4];
-        // stale row maximum, kShift less it (kFar before the first key), partial row sum
+        float o[NT][kBlocks][4];
+        // stale row maximum, kShift less it (kFar before the first key): the same in
+        // all warps; partial row sum
         float m_run[NT][2], nm[NT][2], l_run[NT][2];
         float v_top = __int_as_float(1 << 23);   // power of two that bounds the V scales so far
         float v_inv = pow2_inverse(v_top);
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
 #pragma unroll
-            for (int j = 0; j < kSteps; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
+            for (int j = 0; j < kBlocks; ++j) o[n][j][0] = o[n][j][1] = o[n][j][2] = o[n][j][3] = 0.f;
             m_run[n][0] = m_run[n][1] = -INFINITY;
             nm[n][0] = nm[n][1] = kFar;
             l_run[n][0] = l_run[n][1] = 0.f;
@@ -522,8 +552,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         auto tile = [&](auto edge_c, uint32_t kb, uint32_t vb, int key0) {
             constexpr bool kEdge = decltype(edge_c)::value;
             const int kA = key0 + g8, kB = kA + 8;           // this lane's two keys in S^T
-            const bool clear = kEdge && key0 + 15 >= w.len;
-            if (clear) {
+            if (kEdge && key0 + 15 >= w.len) {
                 // V rows behind the length may hold NaN, and 0 x NaN is NaN
                 constexpr int kChunks = D * L::kElem / 16;
                 for (int e = lane; e < 16 * kChunks; e += 32) {
@@ -532,13 +561,17 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                         asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};"
                                      ::"r"(vb + chunk_off<D, kFmt>(row, e % kChunks)), "r"(0u) : "memory");
                 }
-                __syncwarp();
+                fence_proxy_async_smem();   // the zeros before the next copy into this stage
             }
-            // ---- S^T (16 keys x rows) = K Q^T
-            float s[NT][4];
+            // ---- S^T (16 keys x rows) = K Q^T; 8 rows alone in two halves, which
+            // do not wait for one another
+            float s[NT][4], s_odd[NT][4];
 #pragma unroll
-            for (int n = 0; n < NT; ++n) s[n][0] = s[n][1] = s[n][2] = s[n][3] = 0.f;
-            float ksA = 1.f, ksB = 1.f, vsA = 1.f, vsB = 1.f;
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[n][e] = s_odd[n][e] = 0.f;
+            float ksA = 1.f, ksB = 1.f;
+            [[maybe_unused]] float vsA, vsB;
             if constexpr (kHalf) {
                 const uint32_t sc = sS + st * 2 * L::kScaleBytes + (kw + g8) * 4;
                 ksA = lds32(sc);
@@ -558,7 +591,7 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
                         for (int n = 0; n < NT; ++n) {
                             const uint2 q = lds64(qf + (n * kSteps + 4 * hh + w4) * 256);
-                            mma16<true>(s[n], a0, a1, a2, a3, q.x, q.y);
+                            mma16<true>(NT == 1 && (w4 & 1) ? s_odd[n] : s[n], a0, a1, a2, a3, q.x, q.y);
                         }
                     }
                 }
@@ -570,9 +603,13 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
                         const uint2 q = lds64(qf + (n * kSteps + kk) * 256);
-                        mma16<false>(s[n], a[0], a[1], a[2], a[3], q.x, q.y);
+                        mma16<false>(NT == 1 && (kk & 1) ? s_odd[n] : s[n], a[0], a[1], a[2], a[3], q.x, q.y);
                     }
                 }
+            }
+            if constexpr (NT == 1) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) s[0][e] += s_odd[0][e];
             }
             // ---- mask, online softmax (rows 2 t4, 2 t4 + 1; keys kA, kB).  Element e is
             // (key e / 2, row e % 2); y = score + kShift - stale maximum, in log2 units.
@@ -590,15 +627,59 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                 grow |= vsA > v_top && (!kEdge || kA < w.len);
                 grow |= vsB > v_top && (!kEdge || kB < w.len);
             }
-            if (__any_sync(0xffffffffu, grow)) {
+            // ---- P^T fragments of the warp's keys for all warps; again with new
+            // maxima where a score of any warp asks for them
+            float sum[NT][2];
+            while (true) {
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float pw[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) pw[e] = ex2(y[n][e]);
+                    sum[n][0] = pw[0] + pw[2];
+                    sum[n][1] = pw[1] + pw[3];
+                    uint32_t lo, hi;
+                    if constexpr (kHalf) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            pw[e] *= ((e >> 1) ? vsB : vsA) * v_inv;
+                            // a hidden key's scale may be anything
+                            if (kEdge && y[n][e] == -INFINITY) pw[e] = 0.f;
+                        }
+                        lo = turn8x8(pack_half2(pw[0], pw[1]));
+                        hi = turn8x8(pack_half2(pw[2], pw[3]));
+                    } else {
+                        lo = turn8x8(pack_bf16x2(pw[0], pw[1]));
+                        hi = turn8x8(pack_bf16x2(pw[2], pw[3]));
+                    }
+                    asm volatile("st.shared.v2.u32 [%0], {%1, %2};"
+                                 ::"r"(sP + p_buf + (warp * NT + n) * 256), "r"(lo), "r"(hi) : "memory");
+                }
+                if (!any_of_warps(grow)) break;
                 // a maximum grew by more than kCdRescale, or a V scale past the
                 // bound: take the new ones and bring the sums so far to them
-                float vfac = 1.f;
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        y[n][h] = kEdge && y[n][h] == -INFINITY ? -INFINITY : s[n][h] * (ksA * qc[n][h]);
+                        y[n][2 + h] = kEdge && y[n][2 + h] == -INFINITY ? -INFINITY : s[n][2 + h] * (ksB * qc[n][h]);
+                        float top = fmaxf(y[n][h], y[n][2 + h]);
+#pragma unroll
+                        for (int k = 4; k <= 16; k <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
+                        if (g8 == 0) mx[warp * NT * 8 + n * 8 + 2 * t4 + h] = top;
+                    }
                 if constexpr (kHalf) {
                     float vm = fmaxf(!kEdge || kA < w.len ? vsA : 0.f, !kEdge || kB < w.len ? vsB : 0.f);
 #pragma unroll
                     for (int k = 4; k <= 16; k <<= 1) vm = fmaxf(vm, __shfl_xor_sync(0xffffffffu, vm, k));
-                    const float top = fmaxf(v_top, pow2_at_least(vm));
+                    if (lane == 0) mx[4 * NT * 8 + warp] = vm;
+                }
+                asm volatile("bar.sync 1, 128;" ::: "memory");
+                float vfac = 1.f;
+                if constexpr (kHalf) {
+                    const float* at = mx + 4 * NT * 8;
+                    const float top = fmaxf(v_top, pow2_at_least(fmaxf(fmaxf(at[0], at[1]), fmaxf(at[2], at[3]))));
                     v_inv = pow2_inverse(top);
                     vfac = v_top * v_inv;
                     v_top = top;
@@ -608,84 +689,81 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
                     float alpha[2];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const float xa = kEdge && y[n][h] == -INFINITY ? -INFINITY : s[n][h] * (ksA * qc[n][h]);
-                        const float xb = kEdge && y[n][2 + h] == -INFINITY ? -INFINITY : s[n][2 + h] * (ksB * qc[n][h]);
-                        float mx = fmaxf(xa, xb);
-#pragma unroll
-                        for (int k = 4; k <= 16; k <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, k));
-                        const float m_new = fmaxf(m_run[n][h], mx);
+                        const float* at = mx + n * 8 + 2 * t4 + h;
+                        const float m_new = fmaxf(m_run[n][h], fmaxf(fmaxf(at[0], at[NT * 8]),
+                                                                     fmaxf(at[2 * NT * 8], at[3 * NT * 8])));
                         alpha[h] = m_new == -INFINITY ? 1.f : ex2(m_run[n][h] - m_new);
                         m_run[n][h] = m_new;
                         nm[n][h] = m_new == -INFINITY ? kFar : kShift - m_new;
                         l_run[n][h] *= alpha[h];
                         alpha[h] *= vfac;
-                        y[n][h] = xa + nm[n][h];
-                        y[n][2 + h] = xb + nm[n][h];
+                        y[n][h] += nm[n][h];
+                        y[n][2 + h] += nm[n][h];
                     }
 #pragma unroll
-                    for (int j = 0; j < kSteps; ++j) {
+                    for (int j = 0; j < kBlocks; ++j) {
                         o[n][j][0] *= alpha[0];
                         o[n][j][1] *= alpha[1];
                         o[n][j][2] *= alpha[0];
                         o[n][j][3] *= alpha[1];
                     }
                 }
+                grow = false;
             }
-            vsA *= v_inv;
-            vsB *= v_inv;
-            uint32_t pb[NT][2];
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
-                float pw[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) pw[e] = ex2(y[n][e]);
-                l_run[n][0] += pw[0] + pw[2];
-                l_run[n][1] += pw[1] + pw[3];
-                if constexpr (kHalf) {
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        pw[e] *= (e >> 1) ? vsB : vsA;
-                        // a hidden key's scale may be anything
-                        if (kEdge && y[n][e] == -INFINITY) pw[e] = 0.f;
-                    }
-                    pb[n][0] = turn8x8(pack_half2(pw[0], pw[1]));
-                    pb[n][1] = turn8x8(pack_half2(pw[2], pw[3]));
-                } else {
-                    pb[n][0] = turn8x8(pack_bf16x2(pw[0], pw[1]));
-                    pb[n][1] = turn8x8(pack_bf16x2(pw[2], pw[3]));
-                }
+                l_run[n][0] += sum[n][0];
+                l_run[n][1] += sum[n][1];
             }
-            // ---- O^T (D x rows) += V^T P^T
+            // ---- O^T (the warp's columns x rows) += V^T P^T over the tile's keys
             if constexpr (kHalf) {
 #pragma unroll
-                for (int j = 0; j < kSteps; j += 2) {
-                    uint32_t r[4];
-                    ldsm4_t(chunk_at(vb + v_at, j), r);
+                for (int x = 0; x < 4; x += 2) {
+                    uint32_t r0[4], r1[4];
+                    if constexpr (D == 128) {
+                        ldsm4_t(vb + v_at + x * kRow16, r0);
+                        ldsm4_t(vb + v_at + (x + 1) * kRow16, r1);
+                    } else {
+                        ldsm4_t(vb + v_at + x * kRow16, r0);
+                    }
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        uint32_t a0, a1, a2, a3;   // rows d = 16 (j + u) + 2 g8 (a0, a2) and + 1 (a1, a3)
-                        unpack4_pairs<kFmt>(r[2 * u], a0, a1);
-                        unpack4_pairs<kFmt>(r[2 * u + 1], a2, a3);
+                        // D = 128: key step x + u, columns j of r0 / r1; D = 64: key step x + u in r0
+                        uint2 pf[NT];
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) mma16<true>(o[n][j + u], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+                        for (int n = 0; n < NT; ++n) pf[n] = lds64(sP + p_buf + ((x + u) * NT + n) * 256);
+#pragma unroll
+                        for (int j = 0; j < kBlocks; ++j) {
+                            const uint32_t* rr = D == 128 ? (u ? r1 : r0) + 2 * j : r0 + 2 * u;
+                            uint32_t a0, a1, a2, a3;   // rows d = 2 g8 (a0, a2) and + 1 (a1, a3) of the block
+                            unpack4_pairs<kFmt>(rr[0], a0, a1);
+                            unpack4_pairs<kFmt>(rr[1], a2, a3);
+#pragma unroll
+                            for (int n = 0; n < NT; ++n) mma16<true>(o[n][j], a0, a1, a2, a3, pf[n].x, pf[n].y);
+                        }
                     }
                 }
             } else {
 #pragma unroll
-                for (int j = 0; j < kSteps; ++j) {
-                    uint32_t r[4];
-                    ldsm4_t(chunk_at(vb + v_at, 2 * j), r);
+                for (int x = 0; x < 4; ++x) {
+                    uint2 pf[NT];
 #pragma unroll
-                    for (int n = 0; n < NT; ++n) mma16<false>(o[n][j], r[0], r[1], r[2], r[3], pb[n][0], pb[n][1]);
+                    for (int n = 0; n < NT; ++n) pf[n] = lds64(sP + p_buf + (x * NT + n) * 256);
+#pragma unroll
+                    for (int j = 0; j < kBlocks; ++j) {
+                        uint32_t r[4];
+                        ldsm4_t(chunk_at(vb + v_at, 2 * j) + x * kRow16, r);
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) mma16<false>(o[n][j], r[0], r[1], r[2], r[3], pf[n].x, pf[n].y);
+                    }
                 }
             }
-            if (clear) fence_proxy_async_smem();   // the zeros before the next copy into this stage
+            p_buf ^= L::kPFrag;
         };
 
         for (int i = w.t0; i < w.t1; ++i) {
             ok = ok && mbar_wait(&full[st], phase, abort_flag, kCdSiteFull);
             ok = __all_sync(0xffffffffu, ok);
-            if (!ok) continue;
             const uint32_t kb = sK + st * L::kTileBytes, vb = sV + st * L::kTileBytes;
             const int key0 = i * kCdKeys + kw;               // slot of the warp's first key
             if (__any_sync(0xffffffffu, key0 + 15 > pos_min))
@@ -701,23 +779,17 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
         }
         if (lane == 0) mbar_arrive(&q_empty[buf]);
 
-        // ---- the four warps' parts of the unit, joined in shared memory
+        // ---- row sums over the warps, and the results
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int k = 4; k <= 16; k <<= 1) l_run[n][h] += __shfl_xor_sync(0xffffffffu, l_run[n][h], k);
-        if (g8 == 0) {
-#pragma unroll
-            for (int n = 0; n < NT; ++n)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    ml[warp * 40 + n * 8 + 2 * t4 + h] = m_run[n][h];
-                    ml[warp * 40 + 16 + n * 8 + 2 * t4 + h] = l_run[n][h];
-                }
-            if (t4 == 0) ml[warp * 40 + 32] = v_top;
-        }
+                if (g8 == 0) ml[warp * NT * 8 + n * 8 + 2 * t4 + h] = l_run[n][h];
+            }
+        // (the next unit's writes to ml come after another tile's barrier)
+        asm volatile("bar.sync 1, 128;" ::: "memory");
         // a part that begins before this CTA goes to its slot 2 c, one that ends after it to 2 c + 1
         const bool whole = w.t0 == 0 && w.t1 == w.tiles;
         const int slot = 2 * static_cast<int>(blockIdx.x) + (w.t0 == 0 ? 1 : 0);
@@ -726,82 +798,48 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             const int last = static_cast<int>((end * w.n - 1) / w.total);            // its run
             p.meta[(w.b * p.Hkv + w.h) * p.RB + rb] = make_int2(whole ? -1 : slot, whole ? 1 : last - run + 1);
         }
-        constexpr int kPitch = L::kCols + 4;
-        // 16 threads a row, kCols / 16 columns each
-        constexpr int kPer = L::kCols / 16;
-        const int r = threadIdx.x >> 4, c0 = (threadIdx.x & 15) * kPer;
+        const bool final_rows = whole && p.o_unit == nullptr;
 #pragma unroll
-        for (int n = 0; n < NT; ++n) {
-            float M = -INFINITY, wgt[4], Lsum = 0.f, inv = 0.f;
-            const int row = row0 + n * 8 + r;
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int dh = 0; dh < D / L::kCols; ++dh) {
-                if (n + dh > 0) asm volatile("bar.sync 1, 128;" ::: "memory");   // the previous block has been read
-#pragma unroll
-                for (int jj = 0; jj < L::kCols / 16; ++jj) {
-                    const int j = dh * (L::kCols / 16) + jj;
-                    float* at = merge + (warp * 8 + 2 * t4) * kPitch + jj * 16;
-                    if constexpr (kHalf) {   // o: (d, row 0), (d, row 1), (d + 1, row 0), (d + 1, row 1), d = 2 g8
-                        *reinterpret_cast<float2*>(at + 2 * g8) = make_float2(o[n][j][0], o[n][j][2]);
-                        *reinterpret_cast<float2*>(at + kPitch + 2 * g8) = make_float2(o[n][j][1], o[n][j][3]);
-                    } else {                 // d = g8 and g8 + 8
-                        at[g8] = o[n][j][0];
-                        at[kPitch + g8] = o[n][j][1];
-                        at[g8 + 8] = o[n][j][2];
-                        at[kPitch + g8 + 8] = o[n][j][3];
-                    }
+            for (int h = 0; h < 2; ++h) {
+                const int row = row0 + n * 8 + 2 * t4 + h;
+                const float* at = ml + n * 8 + 2 * t4 + h;
+                const float Lsum = (at[0] + at[NT * 8]) + (at[2 * NT * 8] + at[3 * NT * 8]);
+                // rows without a key: 0; a NaN sum stays NaN
+                const float inv = Lsum == 0.f ? 0.f : (kHalf ? v_top : 1.f) / Lsum;
+                if (row >= R || !ok) continue;
+                const size_t prow = final_rows || whole ? rows_at + row
+                                                        : static_cast<size_t>(slot) * (8 * NT) + n * 8 + 2 * t4 + h;
+                if (warp == 0 && g8 == 0) {
+                    float* lse = final_rows ? p.lse : whole ? p.lse_unit : p.lse_part;
+                    lse[prow] = Lsum == 0.f ? -INFINITY : (m_run[n][h] + log2f(Lsum) - kShift) * kLn2;
                 }
-                asm volatile("bar.sync 1, 128;" ::: "memory");
-                if (dh == 0) {
-                    float top = 0.f;
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        M = fmaxf(M, ml[q * 40 + n * 8 + r]);
-                        if (kHalf) top = fmaxf(top, ml[q * 40 + 32]);
-                    }
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const float mq = ml[q * 40 + n * 8 + r];
-                        wgt[q] = mq == -INFINITY ? 0.f : ex2(mq - M);
-                        Lsum += wgt[q] * ml[q * 40 + 16 + n * 8 + r];
-                        if (kHalf) wgt[q] *= ml[q * 40 + 32] * pow2_inverse(top);
-                    }
-                    // rows without a key: 0; a NaN sum stays NaN
-                    inv = Lsum == 0.f ? 0.f : (kHalf ? top : 1.f) / Lsum;
-                }
-                float acc[kPer];
-#pragma unroll
-                for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q)
-#pragma unroll
-                    for (int e = 0; e < kPer; e += 2) {
-                        const float2 v = *reinterpret_cast<const float2*>(merge + (q * 8 + r) * kPitch + c0 + e);
-                        acc[e] += wgt[q] * v.x;
-                        acc[e + 1] += wgt[q] * v.y;
-                    }
-                const int d = dh * L::kCols + c0;
-                const float lse = d != 0 ? 0.f : (Lsum == 0.f ? -INFINITY : (M + log2f(Lsum) - kShift) * kLn2);
-                if (row < R && ok) {
-                    if (whole && p.o_unit == nullptr) {
-                        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.o) + (rows_at + row) * D + d;
-#pragma unroll
-                        for (int e = 0; e < kPer; e += 2)
-                            *reinterpret_cast<uint32_t*>(out + e) = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
-                        if (d == 0) p.lse[rows_at + row] = lse;
+                for (int j = 0; j < kBlocks; ++j) {
+                    // 8 bits: columns 2 g8, 2 g8 + 1 of the block; bf16: g8, g8 + 8
+                    const int d = (warp * kBlocks + j) * 16;
+                    const float v0 = o[n][j][h] * inv, v1 = o[n][j][2 + h] * inv;
+                    if (final_rows) {
+                        __nv_bfloat16* out = reinterpret_cast<__nv_bfloat16*>(p.o) + prow * D + d;
+                        if constexpr (kHalf) {
+                            *reinterpret_cast<uint32_t*>(out + 2 * g8) = pack_bf16x2(v0, v1);
+                        } else {
+                            out[g8] = __float2bfloat16_rn(v0);
+                            out[g8 + 8] = __float2bfloat16_rn(v1);
+                        }
                     } else {
-                        const size_t prow = whole ? rows_at + row : static_cast<size_t>(slot) * (8 * NT) + n * 8 + r;
                         float* out = (whole ? p.o_unit : p.o_part) + prow * D + d;
-#pragma unroll
-                        for (int e = 0; e < kPer; e += 2)
-                            *reinterpret_cast<float2*>(out + e) = make_float2(acc[e] * inv, acc[e + 1] * inv);
-                        if (d == 0) (whole ? p.lse_unit : p.lse_part)[prow] = lse;
+                        if constexpr (kHalf) {
+                            *reinterpret_cast<float2*>(out + 2 * g8) = make_float2(v0, v1);
+                        } else {
+                            out[g8] = v0;
+                            out[g8 + 8] = v1;
+                        }
                     }
                 }
             }
-        }
         ++unit;
-        asm volatile("bar.sync 1, 128;" ::: "memory");   // ml is free again
     }
     grid_wait();
 }
@@ -943,24 +981,31 @@ cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodePa
     return cudaGetLastError();
 }
 
+template <int D, int kFmt>
+cudaError_t go_rows(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p, bool after_prefix,
+                    cudaStream_t stream) {
+    if (p.rows_cta == 8) return go<D, kFmt, 1>(tk, tv, p, after_prefix, stream);
+    if (p.rows_cta == 16) return go<D, kFmt, 2>(tk, tv, p, after_prefix, stream);
+    return go<D, kFmt, 4>(tk, tv, p, after_prefix, stream);
+}
+
 template <int D>
 cudaError_t go_fmt(int fmt, const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p,
                    bool after_prefix, cudaStream_t stream) {
-    const bool one = p.rows_cta == 8;
-    if (fmt == 0) return one ? go<D, 0, 1>(tk, tv, p, after_prefix, stream) : go<D, 0, 2>(tk, tv, p, after_prefix, stream);
-    if (fmt == 1) return one ? go<D, 1, 1>(tk, tv, p, after_prefix, stream) : go<D, 1, 2>(tk, tv, p, after_prefix, stream);
-    return one ? go<D, 2, 1>(tk, tv, p, after_prefix, stream) : go<D, 2, 2>(tk, tv, p, after_prefix, stream);
+    if (fmt == 0) return go_rows<D, 0>(tk, tv, p, after_prefix, stream);
+    if (fmt == 1) return go_rows<D, 1>(tk, tv, p, after_prefix, stream);
+    return go_rows<D, 2>(tk, tv, p, after_prefix, stream);
 }
 
 }  // namespace
 
-int cache_decode_ctas_per_sm(int D, int fmt) {
-    if (D == 128) return fmt == 0 ? CdLayout<128, 0, 1>::kCtas : CdLayout<128, 1, 1>::kCtas;
-    return fmt == 0 ? CdLayout<64, 0, 1>::kCtas : CdLayout<64, 1, 1>::kCtas;
+int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta) {
+    return rows_cta == 32 || (D == 128 && fmt == 0) ? 2 : 3;
 }
 
-// Measured with 64 sequences of up to 1000 slots (8 rows): 32 us at 0, 25 at 1,
-// 23 at 2; with 48 of up to 8100 (12 rows): 60 at 0, 53 at 2, 51 at 4.
+// Measured with 64 sequences of up to 1000 slots (8 rows, with the join): 32.4 us
+// at 0, 24.6 at 1, 22.1 at 2; with 48 of up to 8100 (12 rows): 51.4 at 1, 47.8
+// at 2, 46.6 at 3, 46.2 at 4.
 int cache_decode_unit_cost(int rows_cta) { return rows_cta == 8 ? 2 : 4; }
 
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,

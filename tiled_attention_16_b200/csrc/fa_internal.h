@@ -254,14 +254,14 @@ struct CacheDecodeParams {
     int2* meta;              // [B * Hkv * RB]: a unit's first slot (-1: undivided) and parts, for each row block
                              // (null: no join follows)
     int B, Hkv, G, Nq, capacity, causal;
-    int rows_cta, RB;        // query rows a CTA holds (8 or 16), row blocks of a K/V head
+    int rows_cta, RB;        // query rows a CTA holds (8, 16 or 32), row blocks of a K/V head
     int n_cta;
     int unit_cost;           // positions a unit counts besides its tiles
     int undivided;           // every unit is a run
     float scale_log2;
 };
 // CTAs of the cache part that fit on an SM at once (shared memory and registers).
-int cache_decode_ctas_per_sm(int D, int fmt);
+int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta);
 int cache_decode_unit_cost(int rows_cta);
 // after_prefix: the prefix kernel is the one ahead of it in the stream.
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
