@@ -68,7 +68,7 @@ FA_API fa_status fa_cache_read(const fa_cache_shape* shape, int N, const int* le
  * slots.  Query i stands at slot len_b - Nq + i: when causal != 0 it sees
  * slots j <= len_b - Nq + i, else all slots below len_b; it always sees the
  * whole prefix.  A key whose score is -inf counts as not seen (as in
- * fa_decode).  A query that sees no key gets o = 0 and lse = -inf.
+ * fa_decode) if its V row is finite.  A query that sees no key gets o = 0 and lse = -inf.
  * Hq % Hkv == 0; Nq >= 1; scale finite and > 0. */
 typedef struct {
     int B, Hq, Hkv, Nq, capacity, n_prefix, D;
@@ -94,8 +94,11 @@ FA_API size_t fa_decode_cache_workspace_bytes(const fa_cache_decode_shape* shape
  * bf16 caches and prefixes P is rounded to bf16 (2^-8).
  * workspace: 256-byte aligned (NULL allowed where 0 bytes are needed), contents
  * on entry do not matter; calls that may overlap need workspaces of their own.
- * o, lse and the workspace share no memory with the inputs.  Codes below a
- * sequence's length must be numbers (the writer's always are). */
+ * o, lse and the workspace share no memory with the inputs.  8-bit codes below a
+ * sequence's length must be numbers (the writer's always are).  bf16 caches and
+ * prefixes may hold infinities and NaNs: a query that sees such a value in a row
+ * of V gets no finite number in its column, whatever the row's weight; a query
+ * that does not see the row is not touched by it. */
 FA_API fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, const void* k_cache,
                                  const void* v_cache, const float* k_scale, const float* v_scale, const int* lens,
                                  const void* k_prefix, const void* v_prefix, void* o, float* lse, void* workspace,

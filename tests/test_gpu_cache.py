@@ -607,3 +607,61 @@ def test_tokens_through_norm_cache_and_decoding():
     assert (np64(hk) == values(kc, ks)[:, :, :int(lens[0])]).all()
     o, lse = A.fwd(hk, hk, hv, causal=True)     # the history as the next chunk's forward takes it
     assert torch.isfinite(o).all() and torch.isfinite(lse).all()
+
+
+POISON = [
+    # B, Hq, Hkv, Nq, cap, D, Np, lens: rows a K/V head in one block of 8, 16, 32 and several; hidden keys in one tile and in more
+    (2, 2, 1, 2, 128, 64, 0, [70, 64]),
+    (2, 8, 2, 3, 200, 128, 0, [65, 130]),
+    (2, 8, 2, 5, 1400, 128, 0, [1398, 3]),
+    (1, 2, 1, 70, 700, 64, 0, [650]),
+    (2, 1, 1, 100, 128, 128, 0, [128, 60]),
+    (2, 4, 2, 4, 700, 64, 300, [699, 2]),
+]
+
+
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,cap,D,Np,lens", POISON)
+def test_poisoned_bf16_values_reach_the_queries_that_see_them_only(B, Hq, Hkv, Nq, cap, D, Np, lens):
+    """Infinities and NaNs in some columns of V rows that the last queries see
+    and the first do not: columns and queries apart from them are as without."""
+    dev = _gpu()
+    kc, vc, _, _ = filled(B, Hkv, cap, D, "bf16", lens, dev)
+    q = rows(B, Hq, Nq, D, 41)
+    pk, pv = ((rows(1, Hkv, Np, D, 5)[0].contiguous(), rows(1, Hkv, Np, D, 6)[0].contiguous()) if Np else (None, None))
+    spots = {}
+    for b, n in enumerate(lens):
+        first = max(n - Nq + 1, 0)             # the first slot that query 0 does not see
+        for slot, col, x in ((n - 1, 3, "inf"), (n - 1, D - 1, "nan"), (first, 17, "-inf"), ((first + n) // 2, 40, "nan")):
+            if first <= slot < n:
+                spots[b, slot, col] = float(x)
+    clean = vc.clone()
+    for (b, slot, col), x in spots.items():
+        vc[b, :, slot, col] = x
+        clean[b, :, slot] = 0
+    got = cache.decode_cache(q, kc, vc, ints(*lens), prefix_k=pk, prefix_v=pv)
+    want = cache.decode_cache(q, kc, clean, ints(*lens), prefix_k=pk, prefix_v=pv)
+    assert A.device_status(dev) == A.FA_OK
+    assert torch.equal(got[1], want[1])        # scores know nothing of V
+    qq, k, v = np64(q), np64(kc), np64(vc)
+    fk, fv = (np.zeros((Hkv, 0, D)),) * 2 if pk is None else (np64(pk), np64(pv))
+    go = np64(got[0])
+    for b, n in enumerate(lens):
+        for i in range(Nq):
+            end = max(n - Nq + i + 1, 0)
+            seen = [s for s in spots if s[0] == b and s[1] < end]
+            if not seen:
+                assert torch.equal(got[0][b, :, i], want[0][b, :, i])
+                continue
+            for h in range(Hq):
+                g = h // (Hq // Hkv)
+                with np.errstate(invalid="ignore"):
+                    ro, _, wt, size = so.decode_rows(qq[b, h, i], np.concatenate([fk[g], k[b, g, :end]]),
+                                                     np.concatenate([fv[g], v[b, g, :end]]), D ** -0.5,
+                                                     np.ones(Np + end, dtype=bool))
+                # 0 * inf is no case here: no weight underflows at these logits
+                assert (np.isnan(go[b, h, i]) == np.isnan(ro)).all() and (np.isinf(go[b, h, i]) == np.isinf(ro)).all()
+                assert (go[b, h, i][np.isinf(ro)] == ro[np.isinf(ro)]).all()
+                fin = np.isfinite(ro)
+                assert fin.sum() >= D - 4
+                tol = (BF * 1.01 + 2 * (D + 16) * 2.0 ** -23 * size + 2.0 ** -18) * wt[fin] + BF * 1.01 * np.abs(ro[fin])
+                assert (np.abs(go[b, h, i][fin] - ro[fin]) <= tol).all()

@@ -338,6 +338,7 @@ fa_status fa_decode_cache(const fa_cache_decode_shape* shape, const void* q, con
     p.lens = lens;
     p.k_scale = k_scale;
     p.v_scale = v_scale;
+    p.v_cache = v_cache;
     p.o_part = f32(pl.o_part);
     p.lse_part = f32(pl.lse_part);
     p.o_unit = s.n_prefix > 0 ? f32(pl.o_unit) : nullptr;

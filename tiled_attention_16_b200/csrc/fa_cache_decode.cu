@@ -84,7 +84,8 @@ struct CdLayout {
     static constexpr int kP = kQScale + 2 * NT * 8 * 4;                 // two tiles' fragments
     static constexpr int kMx = kP + 2 * kPFrag;                         // the warps' row maxima, V scales' maxima
     static constexpr int kMl = kMx + 4 * NT * 8 * 4 + 16;               // and row sums
-    static constexpr int kBar = kMl + 4 * NT * 8 * 4;
+    static constexpr int kBad = kMl + 4 * NT * 8 * 4;                   // two tiles' masks of poisoned V rows, one a warp
+    static constexpr int kBar = kBad + 32;
     static constexpr int kAlloc = kBar + (2 * kStages + 4) * 8 + 16;
     static_assert((kAlloc + 1024) * kCtas <= 228 * 1024, "CTAs must fit");
 };
@@ -127,6 +128,11 @@ __device__ __forceinline__ float lds32(uint32_t addr) {
     float v;
     asm volatile("ld.shared.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
     return v;
+}
+__device__ __forceinline__ float lds_bf16(uint32_t addr) {
+    uint16_t v;
+    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(v) : "r"(addr) : "memory");
+    return __uint_as_float(static_cast<uint32_t>(v) << 16);
 }
 __device__ __forceinline__ uint32_t turn8x8(uint32_t a) {
     uint32_t d;
@@ -319,6 +325,37 @@ __device__ __forceinline__ void cd_drain(uint64_t* bar, uint32_t parity) {
     }
 }
 
+// bf16 V rows that only some of a CTA's query rows see: those that hold an
+// infinity or a NaN among the warp's 16 rows of a tile, `slot0` the first's slot,
+// first <= slot < len.  They are zeroed in the tile, since a hidden key's weight
+// of 0 times them would be NaN, and returned as a mask: the query rows that do see
+// them get them added behind the tile's products.
+template <int D>
+__device__ __forceinline__ uint32_t take_poisoned(uint32_t vb, int kw, int slot0, int first, int len, int lane) {
+    constexpr int kChunks = D * 2 / 16, kRowsAtOnce = 32 / kChunks;
+    uint32_t mask = 0u;
+#pragma unroll
+    for (int r = 0; r < 16; r += kRowsAtOnce) {
+        const int row = r + lane / kChunks;
+        const uint32_t at = vb + chunk_off<D, 0>(kw + row, lane % kChunks);
+        uint32_t top = 0u;
+        if (slot0 + row >= first && slot0 + row < len) {
+            const uint4 w = lds128(at);
+            constexpr uint32_t kAbs = 0x7fff7fffu;
+            top = __vmaxu2(__vmaxu2(w.x & kAbs, w.y & kAbs), __vmaxu2(w.z & kAbs, w.w & kAbs));
+        }
+        const unsigned lanes = __ballot_sync(0xffffffffu, (top >> 16) >= 0x7f80u || (top & 0xffffu) >= 0x7f80u);
+        const unsigned mine = (lanes >> (lane / kChunks * kChunks)) & ((1u << kChunks) - 1u);
+        if (mine)
+            asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at), "r"(0u) : "memory");
+#pragma unroll
+        for (int k = 0; k < kRowsAtOnce; ++k)
+            if ((lanes >> (k * kChunks)) & ((1u << kChunks) - 1u)) mask |= 1u << (r + k);
+    }
+    if (mask) fence_proxy_async_smem();   // the zeros before the next copy into this stage
+    return mask;
+}
+
 // One warp: the B fragments of Q^T for rows row0 .. row0 + 8 NT - 1 of the K/V
 // head whose rows start at rows_at, in the order the MMAs take them (fragment
 // (n, step): 8 bytes a lane), and the rows' factors from the products to
@@ -380,8 +417,11 @@ __device__ __forceinline__ void q_fragments(const CacheDecodeParams& p, uint8_t*
     }
 }
 
-// NT: blocks of 8 query rows a CTA holds.
-template <int D, int kFmt, int NT>
+// NT: blocks of 8 query rows a CTA holds.  kMixed: bf16 V rows that only some
+// query rows see are looked at for infinities and NaNs (single queries, all keys
+// visible and 8 bits have none; it is kept out of their code: 4 sequences of up to
+// 130 slots of 8 heads of 128 take 5.4 us, with it 5.7).
+template <int D, int kFmt, int NT, bool kMixed>
 __global__ void __launch_bounds__(kCdThreads, CdLayout<D, kFmt, NT>::kCtas)
 fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
                        const CacheDecodeParams p) {
@@ -766,10 +806,47 @@ fa_cache_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_con
             ok = __all_sync(0xffffffffu, ok);
             const uint32_t kb = sK + st * L::kTileBytes, vb = sV + st * L::kTileBytes;
             const int key0 = i * kCdKeys + kw;               // slot of the warp's first key
+            // bf16: the tile holds keys that some query rows see and others do not (the same
+            // in all warps).  Double-buffered with P, so its barriers order the masks too.
+            const bool mixed = kMixed && i * kCdKeys + kCdKeys - 1 > pos_min;
+            const uint32_t p_at = sP - lane * 8 + p_buf;     // the tile's P fragments
+            uint32_t* bad = reinterpret_cast<uint32_t*>(smem + L::kBad) + (p_buf ? 4 : 0);
+            if constexpr (kMixed) {
+                if (mixed) {
+                    const uint32_t mask = take_poisoned<D>(vb, kw, key0, pos_min + 1, w.len, lane);
+                    if (lane == 0) bad[warp] = mask;
+                }
+            }
             if (__any_sync(0xffffffffu, key0 + 15 > pos_min))
                 tile(std::true_type{}, kb, vb, key0);
             else
                 tile(std::false_type{}, kb, vb, key0);
+            if constexpr (kMixed) {
+                if (mixed) {
+#pragma unroll 1
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll 1
+                        for (uint32_t left = bad[x]; left; left &= left - 1) {
+                            const int key = __ffs(left) - 1, slot = i * kCdKeys + x * 16 + key;
+                            const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.v_cache) +
+                                                     (static_cast<size_t>(w.b * p.Hkv + w.h) * p.capacity + slot) * D +
+                                                     warp * (kBlocks * 16) + g8;
+                            const uint32_t at = p_at + x * NT * 256 + (key >> 1 & 3) * 8 + (key >> 3) * 4 + (key & 1) * 2;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    if (slot > pos[n][h]) continue;
+                                    const float pw = lds_bf16(at + n * 256 + (2 * t4 + h) * 32);
+#pragma unroll
+                                    for (int j = 0; j < kBlocks; ++j) {
+                                        o[n][j][h] = fmaf(pw, __bfloat162float(v[j * 16]), o[n][j][h]);
+                                        o[n][j][2 + h] = fmaf(pw, __bfloat162float(v[j * 16 + 8]), o[n][j][2 + h]);
+                                    }
+                                }
+                        }
+                }
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(&empty[st]);
             if (++st == kStages) {
@@ -968,10 +1045,10 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
     if (lane == 0) p.lse[gr] = Z == 0.f ? -INFINITY : M + logf(Z);
 }
 
-template <int D, int kFmt, int NT>
+template <int D, int kFmt, int NT, bool kMixed>
 cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p, bool after_prefix,
                cudaStream_t stream) {
-    auto kern = fa_cache_decode_kernel<D, kFmt, NT>;
+    auto kern = fa_cache_decode_kernel<D, kFmt, NT, kMixed>;
     static SmemOptIn opt_in;
     const cudaError_t e = opt_in.set(reinterpret_cast<const void*>(kern), CdLayout<D, kFmt, NT>::kAlloc);
     if (e != cudaSuccess) return e;
@@ -981,20 +1058,22 @@ cudaError_t go(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodePa
     return cudaGetLastError();
 }
 
-template <int D, int kFmt>
+template <int D, int kFmt, bool kMixed>
 cudaError_t go_rows(const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p, bool after_prefix,
                     cudaStream_t stream) {
-    if (p.rows_cta == 8) return go<D, kFmt, 1>(tk, tv, p, after_prefix, stream);
-    if (p.rows_cta == 16) return go<D, kFmt, 2>(tk, tv, p, after_prefix, stream);
-    return go<D, kFmt, 4>(tk, tv, p, after_prefix, stream);
+    if (p.rows_cta == 8) return go<D, kFmt, 1, kMixed>(tk, tv, p, after_prefix, stream);
+    if (p.rows_cta == 16) return go<D, kFmt, 2, kMixed>(tk, tv, p, after_prefix, stream);
+    return go<D, kFmt, 4, kMixed>(tk, tv, p, after_prefix, stream);
 }
 
 template <int D>
 cudaError_t go_fmt(int fmt, const CUtensorMap& tk, const CUtensorMap& tv, const CacheDecodeParams& p,
                    bool after_prefix, cudaStream_t stream) {
-    if (fmt == 0) return go_rows<D, 0>(tk, tv, p, after_prefix, stream);
-    if (fmt == 1) return go_rows<D, 1>(tk, tv, p, after_prefix, stream);
-    return go_rows<D, 2>(tk, tv, p, after_prefix, stream);
+    if (fmt == 0)
+        return p.causal && p.Nq > 1 ? go_rows<D, 0, true>(tk, tv, p, after_prefix, stream)
+                                    : go_rows<D, 0, false>(tk, tv, p, after_prefix, stream);
+    if (fmt == 1) return go_rows<D, 1, false>(tk, tv, p, after_prefix, stream);
+    return go_rows<D, 2, false>(tk, tv, p, after_prefix, stream);
 }
 
 }  // namespace

@@ -248,6 +248,7 @@ struct CacheDecodeParams {
     float* lse;              // fp32 [B,Hq,Nq]
     const int* lens;
     const float *k_scale, *v_scale;
+    const void* v_cache;     // read directly where a bf16 row holds an infinity or a NaN
     float *o_part, *lse_part;  // parts of units shared by CTAs: slots 2 c, 2 c + 1 of rows_cta rows each
     float *o_unit, *lse_unit;  // [B*Hq*Nq, D], [B*Hq*Nq]: undivided units' results for the merge with the
                                // prefix (null without one: they go to o and lse)
