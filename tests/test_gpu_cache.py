@@ -665,3 +665,53 @@ def test_poisoned_bf16_values_reach_the_queries_that_see_them_only(B, Hq, Hkv, N
                 assert fin.sum() >= D - 4
                 tol = (BF * 1.01 + 2 * (D + 16) * 2.0 ** -23 * size + 2.0 ** -18) * wt[fin] + BF * 1.01 * np.abs(ro[fin])
                 assert (np.abs(go[b, h, i][fin] - ro[fin]) <= tol).all()
+
+
+FAR_POISON = [
+    # cap, len, Np, poisoned slot (own if None: the prefix's), rows a K/V head: undivided, divided, and both behind a prefix
+    (500, 490, 0, 5, 2),
+    (4096, 4000, 0, 5, 2),
+    (4096, 4000, 0, 5, 40),
+    (300, 300, 700, 5, 2),
+    (300, 300, 700, None, 2),
+    (2000, 1999, 400, 5, 150),
+    (2000, 1999, 400, None, 150),
+]
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("cap,n,Np,at,Hq", FAR_POISON)
+def test_poison_far_below_the_largest_score_is_not_lost(fmt, D, cap, n, Np, at, Hq):
+    """A visible V row of NaN whose score lies 256 below others, more than a
+    weight in fp32 can show: 0 times NaN is NaN however the keys are divided."""
+    dev = _gpu()
+    kc, vc, ks, vs = new_cache(1, 1, cap, D, fmt, dev)
+    heavy = torch.zeros(1, 1, n, D)
+    g = torch.Generator().manual_seed(3)
+    heavy[..., 1:] = 0.1 * torch.randn(1, 1, n, D - 1, generator=g)
+    pk, pv = ((rows(1, 1, Np, D, 5, sigma=0.1)[0].contiguous(), rows(1, 1, Np, D, 6)[0].contiguous()) if Np else (None, None))
+    if Np and at is not None:
+        pk[:, 50:, 0] = 16 * D ** 0.5          # the prefix outweighs the sequence's own keys
+    else:
+        heavy[:, :, n - 100:, 0] = 16 * D ** 0.5
+    cache.cache_write(heavy.to(torch.bfloat16).to(dev), rows(1, 1, n, D, 2), kc, vc, ints(0), k_scale=ks, v_scale=vs)
+    q = rows(1, Hq, 1, D, 3, sigma=0.1).clone()
+    q[..., 0] = 16
+    clean = cache.decode_cache(q, kc, vc, ints(n), ks, vs, pk, pv)
+    assert torch.isfinite(clean[0]).all()
+    if at is None:
+        pv[0, 5, 7] = float("nan")
+    elif fmt == "bf16":
+        vc[0, 0, at, 7] = float("nan")
+    else:
+        vs[0, 0, at] = float("nan")
+    o, lse = cache.decode_cache(q, kc, vc, ints(n), ks, vs, pk, pv)
+    assert A.device_status(dev) == A.FA_OK
+    assert torch.equal(lse, clean[1])
+    bad = torch.zeros(D, dtype=torch.bool, device=dev)
+    if at is None or fmt == "bf16":
+        bad[7] = True
+    else:
+        bad[:] = True
+    assert torch.isnan(o[..., bad]).all() and torch.equal(o[..., ~bad], clean[0][..., ~bad])

@@ -986,7 +986,9 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
         for (int k = 16; k; k >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, k));
         const float m_new = fmaxf(M, top);
         const float a = m_new == -INFINITY ? 1.f : expf(M - m_new);
-        const float e = lse == -INFINITY ? 0.f : expf(lse - m_new);
+        // -1: a part without a key, whose o is to be left alone; a weight that only
+        // underflows to 0 still meets its o, so that a NaN there stays one
+        const float e = lse == -INFINITY ? -1.f : expf(lse - m_new);
         M = m_new;
         Z = Z * a;
 #pragma unroll
@@ -997,7 +999,7 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
             const float w = __shfl_sync(0xffffffffu, e, j);
             const float* oj = reinterpret_cast<const float*>(
                 __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(o), j));
-            Z += w;
+            Z = w < 0.f ? Z : Z + w;
             float v[kPer];
             if constexpr (kPer == 4) {
                 const float4 x = __ldcg(reinterpret_cast<const float4*>(oj) + lane);
@@ -1010,9 +1012,8 @@ fa_cache_combine_kernel(const CacheDecodeParams p, const PrefixParams f, int n_r
                 v[0] = x.x;
                 v[1] = x.y;
             }
-            // a part without a key may not have written its o
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) acc[i] = w == 0.f ? acc[i] : fmaf(w, v[i], acc[i]);
+            for (int i = 0; i < kPer; ++i) acc[i] = w < 0.f ? acc[i] : fmaf(w, v[i], acc[i]);
         }
     }
     if constexpr (kWarps > 1) {
