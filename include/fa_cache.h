@@ -41,7 +41,7 @@ extern "C" {
 
 /* D = 64 or 128 (FA_ERR_UNSUPPORTED otherwise); capacity >= 1, a multiple of
  * 4 for the 8-bit formats (the rows of scales start on 16 bytes); B * Hkv <=
- * 65535. */
+ * 65535.  A write or read of N rows a head takes B * Hkv * N <= 2^31 - 1. */
 typedef struct {
     int B, Hkv, capacity, D;
     int format;
@@ -68,8 +68,14 @@ FA_API fa_status fa_cache_read(const fa_cache_shape* shape, int N, const int* le
  * slots.  Query i stands at slot len_b - Nq + i: when causal != 0 it sees
  * slots j <= len_b - Nq + i, else all slots below len_b; it always sees the
  * whole prefix.  A key whose score is -inf counts as not seen (as in
- * fa_decode) if its V row is finite.  A query that sees no key gets o = 0 and lse = -inf.
- * Hq % Hkv == 0; Nq >= 1; scale finite and > 0. */
+ * fa_decode) if its V row is finite.  A query that sees no key gets o = 0 and
+ * lse = -inf.
+ * Hq % Hkv == 0; Nq >= 1; scale finite and > 0.  Beyond the cache's limits:
+ * B * Hq * Nq <= FA_CACHE_MAX_ROWS; capacity <= 2^31 - 64, and with R = Hq / Hkv
+ * * Nq, B * Hkv * (ceil(capacity / 64) + (R <= 8 ? 2 : 4)) <= 2^31 - 1; n_prefix
+ * <= 2^31 - 256, and Hkv * ceil(B * R / U) * ceil(n_prefix / 128) <= 2^31 - 1 with
+ * U = 128 for B * R <= 128, else 256. */
+#define FA_CACHE_MAX_ROWS (1 << 24)
 typedef struct {
     int B, Hq, Hkv, Nq, capacity, n_prefix, D;
     int format;

@@ -47,8 +47,8 @@ typedef struct {
 } fa_rows;
 
 /* D = 64 or 128 (FA_ERR_UNSUPPORTED otherwise); Hq and Hkv are free of each
- * other; 0 <= rotary_dim <= D, a multiple of 8; eps finite and > 0;
- * weight_bf16: the weights are bf16, else fp32. */
+ * other, Hq + Hkv <= 65535; B * N <= 2^31 - 1; 0 <= rotary_dim <= D, a multiple
+ * of 8; eps finite and > 0; weight_bf16: the weights are bf16, else fp32. */
 typedef struct {
     int B, Hq, Hkv, N, D;
     int rotary_dim, interleaved;

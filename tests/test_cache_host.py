@@ -280,3 +280,43 @@ def test_headers_compile_as_c99(tmp_path):
     assert r.returncode == 0, r.stderr
     r = subprocess.run([str(exe)], capture_output=True, text=True, timeout=120)
     assert r.returncode == 0 and r.stdout.strip() == "ok", r.stderr
+
+
+# ---- the limits of a shape, just inside and just past each
+
+LIMITS = [
+    # rows
+    (dict(B=1 << 10, Hq=1 << 10, Hkv=2, Nq=16, capacity=4), dict(B=1 << 10, Hq=(1 << 10) + 2, Hkv=2, Nq=16, capacity=4)),
+    (dict(B=1, Hq=1, Hkv=1, Nq=1 << 24), dict(B=1, Hq=1, Hkv=1, Nq=(1 << 24) + 1)),
+    # slots of one sequence
+    (dict(B=1, Hq=1, Hkv=1, capacity=(1 << 31) - 64), dict(B=1, Hq=1, Hkv=1, capacity=(1 << 31) - 60)),
+    (dict(B=1, Hq=1, Hkv=1, format=0, capacity=(1 << 31) - 64), dict(B=1, Hq=1, Hkv=1, format=0, capacity=(1 << 31) - 63)),
+    # key tiles of all sequences' heads and 2 (up to 8 rows a head) or 4 for each: 65535 x 32768 is 2^31 - 32768
+    (dict(B=65535, Hq=8, Hkv=1, capacity=32766 * 64), dict(B=65535, Hq=8, Hkv=1, capacity=32766 * 64 + 4)),
+    (dict(B=65535, Hq=9, Hkv=1, capacity=32764 * 64), dict(B=65535, Hq=9, Hkv=1, capacity=32764 * 64 + 4)),
+    # the prefix: keys, and key tiles of all heads' row tiles of 128 and of 256
+    (dict(B=1, Hq=1, Hkv=1, n_prefix=(1 << 31) - 256), dict(B=1, Hq=1, Hkv=1, n_prefix=(1 << 31) - 255)),
+    (dict(B=1, Hq=65535, Hkv=65535, n_prefix=32768 * 128), dict(B=1, Hq=65535, Hkv=65535, n_prefix=32768 * 128 + 1)),
+    (dict(B=257, Hq=2, Hkv=1, n_prefix=(1 << 31) // 4), dict(B=257, Hq=2, Hkv=1, Nq=512, n_prefix=(1 << 31) // 4)),
+    # few slots of many rows, many slots of few: no product of the two counts
+    (dict(B=8, Hq=128, Hkv=1, Nq=128, D=64, capacity=1 << 20), dict(B=8, Hq=128, Hkv=1, Nq=1 << 15, D=64, capacity=1 << 20)),
+    (dict(B=8, Hq=128, Hkv=1, Nq=128, n_prefix=1 << 21), dict(B=8, Hq=128, Hkv=1, Nq=128, n_prefix=1 << 30)),
+]
+
+
+@pytest.mark.parametrize("inside,past", LIMITS)
+def test_decode_limits(inside, past):
+    pre = lambda kw: dict(pk=P, pv=P) if kw.get("n_prefix") else {}  # noqa: E731
+    assert call_decode(dshape(**past), **pre(past)) == BAD
+    if not torch.cuda.is_available():
+        assert no_gpu(call_decode(dshape(**inside), **pre(inside)))
+
+
+def test_write_read_and_rope_limits():
+    assert call_write(cshape(B=1, Hkv=2), N=1 << 30) == BAD and call_write(cshape(B=3, Hkv=1), N=715827883) == BAD
+    assert call_rope(rshape(Hq=65535, Hkv=1)) == BAD and call_rope(rshape(B=1 << 16, N=1 << 15)) == BAD
+    if not torch.cuda.is_available():
+        assert no_gpu(call_write(cshape(B=1, Hkv=2), N=(1 << 30) - 1)) and no_gpu(call_write(cshape(B=3, Hkv=1), N=715827882))
+        assert no_gpu(call_read(cshape(B=65535, Hkv=1, capacity=32768), N=32768))
+        assert call_read(cshape(B=65535, Hkv=1, capacity=32772), N=32769) == BAD
+        assert no_gpu(call_rope(rshape(Hq=65534, Hkv=1))) and no_gpu(call_rope(rshape(B=(1 << 16) - 1, N=1 << 15)))

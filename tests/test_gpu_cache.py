@@ -715,3 +715,40 @@ def test_poison_far_below_the_largest_score_is_not_lost(fmt, D, cap, n, Np, at, 
     else:
         bad[:] = True
     assert torch.isnan(o[..., bad]).all() and torch.equal(o[..., ~bad], clean[0][..., ~bad])
+
+
+def test_many_rows_over_a_long_cache():
+    """131072 query rows of 16384 a K/V head, caches of 2^20 slots: far more row
+    blocks than CTAs fit at once, each over all of its sequence."""
+    dev = _gpu()
+    B, Hq, Nq, cap, D = 8, 128, 128, 1 << 20, 64
+    lens = [700, 130, 0, 1, 64, 5, 128, 999]
+    kc, vc, ks, vs = filled(B, 1, cap, D, "e4m3", lens, dev)
+    q = rows(B, Hq, Nq, D, 3)
+    o, lse = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs)
+    assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
+    near = [t[:, :, :1000] for t in (kc, vc, ks, vs)]
+    check_decode(q[:, 5::32], *near, ints(*lens), (o[:, 5::32], lse[:, 5::32]))
+
+
+def test_many_rows_behind_a_long_prefix():
+    """131072 query rows over a prefix of 2^21 + 100 keys.  A part adds up to
+    16385 key tiles one after another, so sums in fp32 are off by up to 16385
+    2^-24 of their magnitudes (twice: numerator and sum)."""
+    dev = _gpu()
+    B, Hq, Nq, D, Np = 8, 128, 128, 64, (1 << 21) + 100
+    kc, vc, ks, vs = filled(B, 1, 4, D, "int8", [4] * B, dev)
+    q = rows(B, Hq, Nq, D, 3)
+    pk, pv = rows(1, 1, Np, D, 5)[0].contiguous(), rows(1, 1, Np, D, 6)[0].contiguous()
+    o, lse = cache.decode_cache(q, kc, vc, ints(*[4] * B), ks, vs, pk, pv)
+    assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
+    k, v, fk, fv = values(kc, ks), values(vc, vs), np64(pk)[0], np64(pv)[0]
+    sums = 16385 * 2.0 ** -24
+    for b, h, i in ((0, 0, 0), (3, 64, 126), (7, 127, 127)):
+        own = max(4 - Nq + i + 1, 0)
+        ro, rl, wt, size = so.decode_rows(np64(q[b, h, i]), np.concatenate([fk, k[b, 0, :own]]),
+                                          np.concatenate([fv, v[b, 0, :own]]), D ** -0.5, np.ones(Np + own, dtype=bool))
+        ds = (D + 16) * 2.0 ** -23 * size
+        tol = (BF * 1.01 + 2 * ds + 2 * sums + 2.0 ** -18) * wt + BF * 1.01 * np.abs(ro)
+        assert (np.abs(np64(o[b, h, i]) - ro) <= tol).all()
+        assert abs(float(lse[b, h, i]) - rl) <= ds + sums + 2.0 ** -18 + 2.0 ** -22 * abs(rl)

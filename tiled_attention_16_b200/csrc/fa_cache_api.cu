@@ -110,6 +110,14 @@ bool cache_pointers_ok(int format, const void* kc, const void* vc, const float* 
     return format == FA_CACHE_BF16 || (aligned16(ks) && aligned16(vs));
 }
 
+// Query rows of a K/V head a CTA of the cache part holds, of R.
+// 8 sequences of 32K slots of 8 heads of 128, with 32 rows a CTA and with twice
+// 16: 24 int8 rows 142 and 170 us, 32 rows e4m3 153 and 150, bf16 168 and 188.
+int rows_of_cta(long long R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
+// Rows of a unit of the prefix part, of head_rows: two row tiles share the key
+// tiles where there are two.
+int rows_of_prefix_unit(long long head_rows) { return head_rows > kTileM ? 2 * kTileM : kTileM; }
+
 fa_status check_decode(const fa_cache_decode_shape* s) {
     if (!s) return FA_ERR_INVALID_ARG;
     const fa_cache_shape c{s->B, s->Hkv, s->capacity, s->D, s->format};
@@ -117,11 +125,16 @@ fa_status check_decode(const fa_cache_decode_shape* s) {
     if (st != FA_OK && st != FA_ERR_UNSUPPORTED) return st;
     if (s->Hq < 1 || s->Nq < 1 || s->n_prefix < 0 || s->Hq % s->Hkv != 0) return FA_ERR_INVALID_ARG;
     if (!std::isfinite(s->scale) || !(s->scale > 0.f)) return FA_ERR_INVALID_ARG;
-    const long long rows = static_cast<long long>(s->B) * s->Hq * s->Nq;
-    if (rows > (1LL << 24)) return FA_ERR_INVALID_ARG;
-    // the kernels number the key tiles of all row blocks with 32 bits
-    if (rows * ((s->capacity + 63LL) / 64 + 8) > kIntMax || rows * ((s->n_prefix + 127LL) / 128) > kIntMax)
-        return FA_ERR_INVALID_ARG;
+    const long long heads = static_cast<long long>(s->B) * s->Hq;
+    if (heads > FA_CACHE_MAX_ROWS || heads * s->Nq > FA_CACHE_MAX_ROWS) return FA_ERR_INVALID_ARG;
+    // What the kernels number with 32 bits: slots and keys (rounded up to tiles),
+    // the positions that all units cover, the prefix's key tiles of all its units.
+    if (s->capacity > kIntMax - 63 || s->n_prefix > kIntMax - 255) return FA_ERR_INVALID_ARG;
+    const long long R = static_cast<long long>(s->Hq / s->Hkv) * s->Nq, head_rows = s->B * R;
+    const long long units = static_cast<long long>(s->B) * s->Hkv;
+    if (units * ((s->capacity + 63LL) / 64 + cache_decode_unit_cost(rows_of_cta(R))) > kIntMax) return FA_ERR_INVALID_ARG;
+    const int unit = rows_of_prefix_unit(head_rows);
+    if (s->Hkv * ((head_rows + unit - 1) / unit) * ((s->n_prefix + kTileN - 1LL) / kTileN) > kIntMax) return FA_ERR_INVALID_ARG;
     return st;
 }
 
@@ -145,9 +158,7 @@ struct DecodeCachePlan {
 DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
     DecodeCachePlan pl{};
     const int R = s.Hq / s.Hkv * s.Nq;
-    // 8 sequences of 32K slots of 8 heads of 128, with 32 rows a CTA and with twice
-    // 16: 24 int8 rows 142 and 170 us, 32 rows e4m3 153 and 150, bf16 168 and 188.
-    pl.rows_cta = R <= 8 ? 8 : R <= 16 ? 16 : 32;
+    pl.rows_cta = rows_of_cta(R);
     pl.RB = (R + pl.rows_cta - 1) / pl.rows_cta;
     // runs of tiles, and RB CTAs to each
     const long long units = static_cast<long long>(s.B) * s.Hkv;
@@ -158,8 +169,8 @@ DecodeCachePlan decode_cache_plan(const fa_cache_decode_shape& s, int sms) {
     const long long rows = static_cast<long long>(s.B) * s.Hq * s.Nq;
     if (s.n_prefix > 0) {
         const long long head_rows = static_cast<long long>(s.B) * R;
-        const bool two = head_rows > kTileM;     // two row tiles share the key tiles
-        pl.rows_unit = two ? 2 * kTileM : kTileM;
+        pl.rows_unit = rows_of_prefix_unit(head_rows);
+        const bool two = pl.rows_unit == 2 * kTileM;
         pl.n_rowtiles = static_cast<int>((head_rows + pl.rows_unit - 1) / pl.rows_unit);
         pl.n_tiles = (s.n_prefix + kTileN - 1) / kTileN;
         const long long units = static_cast<long long>(s.Hkv) * pl.n_rowtiles, tiles = units * pl.n_tiles;
