@@ -320,3 +320,19 @@ def test_write_read_and_rope_limits():
         assert no_gpu(call_read(cshape(B=65535, Hkv=1, capacity=32768), N=32768))
         assert call_read(cshape(B=65535, Hkv=1, capacity=32772), N=32769) == BAD
         assert no_gpu(call_rope(rshape(Hq=65534, Hkv=1))) and no_gpu(call_rope(rshape(B=(1 << 16) - 1, N=1 << 15)))
+
+
+def test_package_imports_where_torch_has_no_cuda():
+    """The workloads and the oracle's users import the package on machines
+    whose torch was built without CUDA, and so without these names."""
+    import subprocess
+    import sys
+    from tiled_attention_16_b200.build import ROOT
+    code = ("import torch\n"
+            "for n in [n for n in dir(torch._C) if n.startswith('_cuda_')]: delattr(torch._C, n)\n"
+            "import tiled_attention_16_b200 as t\n"
+            "from tiled_attention_16_b200 import cache, rope, workloads\n"
+            "try:\n    t.qk_norm_rope(*[torch.zeros(1, 1, 1, 64, dtype=torch.bfloat16)] * 2, *[torch.zeros(64)] * 2, None)\n"
+            "except ValueError as e:\n    print('ok', e)\n")
+    r = subprocess.run([sys.executable, "-c", code], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.startswith("ok"), r.stderr

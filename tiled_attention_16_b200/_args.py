@@ -10,8 +10,11 @@ import torch
 
 from .attention import _check, _same_device
 
-#: The current stream of a device as an integer (torch.cuda.current_stream(...).cuda_stream without the object).
-raw_stream = torch._C._cuda_getCurrentRawStream
+
+def raw_stream(index: int) -> int:
+    """The current stream of a device as an integer (torch.cuda.current_stream(...).cuda_stream
+    without the object).  The name is looked up at the call: a torch without CUDA has none."""
+    return torch._C._cuda_getCurrentRawStream(index)
 
 
 def want(t, name: str, shape: tuple, dtype, first: torch.Tensor) -> None:
