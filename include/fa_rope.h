@@ -18,11 +18,12 @@
  *     h = g w,         dx_d = r (h_d - x_d r mean(h x r)),
  * with x read again and r recomputed from it.
  *
- * Sums and norms are in fp32, angles and their reduction modulo a turn in
- * fp64 (exact enough for every int position); results are rounded to bf16
- * once, dw stays fp32.  A row whose sum of squares is beyond fp32 (values
- * above about 1e18) is out of range.  dw is summed in a fixed order: repeated
- * calls are bitwise equal.
+ * Sums and norms are in fp32.  An angle is reduced modulo a turn in 64-bit
+ * integers, to within 2^-31 + 2^-106 |position * inv_freq| of a turn whatever
+ * the position, and its cos and sin are fp32's (of the angle rounded to fp32:
+ * about 1e-7 rad).  Results are rounded to bf16 once, dw stays fp32.  A row
+ * whose sum of squares is beyond fp32 (values above about 1e18) is out of range.
+ * dw is summed in a fixed order: repeated calls are bitwise equal.
  *
  * Ownership, streams, errors: as in fa.h.  Calls are asynchronous on
  * `stream`, allocate nothing and can be captured into a CUDA graph.

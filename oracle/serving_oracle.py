@@ -14,6 +14,30 @@ def rope_angles(positions, inv_freq):
     return np.asarray(positions, dtype=np.float64)[..., None] * _f64(inv_freq)
 
 
+def reduced_angles(positions, inv_freq):
+    """rope_angles modulo a turn, in [-pi, pi], for products of any size: the
+    turns are formed in integers of 2^-400."""
+    one = 1 << 400
+
+    def arctan_inverse(x):   # Machin: pi = 16 arctan(1/5) - 4 arctan(1/239)
+        term, total, n = one // x, 0, 1
+        while term:
+            total += term // n if n % 4 == 1 else -(term // n)
+            term //= x * x
+            n += 2
+        return total
+
+    pi = 4 * (4 * arctan_inverse(5) - arctan_inverse(239))
+    out = np.zeros(np.shape(positions) + (len(inv_freq),))
+    for i, f in enumerate(np.asarray(inv_freq, dtype=np.float64).tolist()):
+        num, den = f.as_integer_ratio()
+        rate = one * one * num // (2 * pi * den)
+        for at in np.ndindex(*np.shape(positions)):
+            turn = rate * int(positions[at]) % one
+            out[at + (i,)] = 2 * np.pi * ((turn - one if 2 * turn >= one else turn) / one)
+    return out
+
+
 def rotate(u, ang, interleaved: bool, inverse: bool = False):
     """Rows u [..., D] with the pairs of the first 2 * ang.shape[-1] values turned by ang [..., R / 2]."""
     y = np.array(u, dtype=np.float64)
@@ -26,20 +50,20 @@ def rotate(u, ang, interleaved: bool, inverse: bool = False):
     return y
 
 
-def norm_rope(x, w, inv_freq, positions, eps: float, interleaved: bool):
+def norm_rope(x, w, inv_freq, positions, eps: float, interleaved: bool, angles=rope_angles):
     """x [B,H,N,D], w [D], positions [B,N] -> (y, u): rotated and unrotated normed rows."""
     x, w = _f64(x), _f64(w)
     u = x / np.sqrt((x * x).mean(-1, keepdims=True) + eps) * w
-    return rotate(u, rope_angles(positions, inv_freq)[:, None], interleaved), u
+    return rotate(u, angles(positions, inv_freq)[:, None], interleaved), u
 
 
-def norm_rope_backward(dy, x, w, inv_freq, positions, eps: float, interleaved: bool):
+def norm_rope_backward(dy, x, w, inv_freq, positions, eps: float, interleaved: bool, angles=rope_angles):
     """(dx, dw, size_dx, size_dw): gradients and, for error bounds, the sums of
     magnitudes that they come from."""
     dy, x, w = _f64(dy), _f64(x), _f64(w)
     r = 1.0 / np.sqrt((x * x).mean(-1, keepdims=True) + eps)
     xh = x * r
-    ang = rope_angles(positions, inv_freq)[:, None]
+    ang = angles(positions, inv_freq)[:, None]
     g = rotate(dy, ang, interleaved, inverse=True)
     dw = (g * xh).sum((0, 1, 2))
     h = g * w

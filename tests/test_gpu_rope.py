@@ -274,3 +274,30 @@ def test_training_step_with_attention():
     rdk, rdkw, _, _ = so.norm_rope_backward(gk, np64(k), np64(kw), np64(inv), p, 1e-6, False)
     for a, b in ((got[0], rdq), (got[1], rdk), (got[2], rdqw), (got[3], rdkw), (dv, gv)):
         assert np.linalg.norm(np64(a) - b) <= 2e-2 * np.linalg.norm(b)
+
+
+@pytest.mark.parametrize("inter", [False, True])
+@pytest.mark.parametrize("top", [1.0, 1e3, 3e5, 1e17, 3e38])
+def test_angles_of_any_size(top, inter):
+    """Frequencies far from 1 at the largest positions, against angles reduced
+    in integers: within 2^-31 + 2^-106 |angle| of a turn, then fp32."""
+    dev = _gpu()
+    D, rot = 64, 64
+    q, k, qw, kw, _, _, dq, dk = make(2, 3, 2, 8, D, rot, seed=21)
+    inv = torch.from_numpy(np.geomspace(1e-6, top, rot // 2).astype(np.float32)).to(dev)
+    pos = torch.tensor([[0, 1, -1, 77, 1000001, -123456789, 2 ** 31 - 1, -(2 ** 31)],
+                        [3, 2 ** 30, 5, 2 ** 31 - 2, 2, 65537, 12345, 4096]], dtype=torch.int32, device=dev)
+    eps = 1e-6
+    got = rope.qk_norm_rope(q, k, qw, kw, inv, positions=pos, eps=eps, interleaved=inter)
+    grads = rope.qk_norm_rope_bwd(dq, dk, q, k, qw, kw, inv, positions=pos, eps=eps, interleaved=inter)
+    far = 2 * np.pi * (2.0 ** -31 + 2.0 ** -106 * float(inv.max()) * 2.0 ** 31)
+    assert far < 2.0 ** -10 or top > 1e30
+    slack = 32 * U + 2.0 ** -22 + min(far, 2.0)
+    for x, w, dy, y, dx, dw in ((q, qw, dq, got[0], grads[0], grads[2]), (k, kw, dk, got[1], grads[1], grads[3])):
+        args = (np64(x), np64(w), np64(inv), pos.cpu().numpy(), eps, inter, so.reduced_angles)
+        ref, u = so.norm_rope(*args)
+        size = np.abs(u).max(-1, keepdims=True)
+        assert (np.abs(np64(y) - ref) <= BF * np.abs(ref) * (1 + BF) + 2 * slack * size).all()
+        rdx, rdw, sdx, sdw = so.norm_rope_backward(np64(dy), *args)
+        assert (np.abs(np64(dx) - rdx) <= BF * np.abs(rdx) * (1 + BF) + slack * sdx + 2.0 ** -133).all()
+        assert (np.abs(np64(dw) - rdw) <= ((2 * 8 * 3 + 32) * U + slack) * sdw).all()
