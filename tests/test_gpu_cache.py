@@ -752,3 +752,28 @@ def test_many_rows_behind_a_long_prefix():
         tol = (BF * 1.01 + 2 * ds + 2 * sums + 2.0 ** -18) * wt + BF * 1.01 * np.abs(ro)
         assert (np.abs(np64(o[b, h, i]) - ro) <= tol).all()
         assert abs(float(lse[b, h, i]) - rl) <= ds + sums + 2.0 ** -18 + 2.0 ** -22 * abs(rl)
+
+
+PREFIX_DIVIDED = [
+    # B, Hq, Hkv, Nq, cap, D, Np, lens, causal: caches whose heads several CTAs share, behind a prefix, 5 to 100 rows a head
+    (2, 16, 1, 4, 700, 128, 200, [700, 3], True),               # two row blocks; one row tile of the prefix, full
+    (3, 33, 1, 1, 1032, 64, 300, [1031, 0, 513], True),         # a row block of one row
+    (2, 9, 1, 1, 600, 64, 130, [600, 599], False),
+    (5, 32, 2, 2, 900, 128, 500, [900, 1, 64, 65, 899], True),  # two row tiles share the prefix's keys
+    (2, 50, 1, 2, 520, 128, 129, [519, 2], False),              # four row blocks
+    (1, 12, 4, 3, 3000, 64, 1000, [2999], True),
+    (40, 10, 2, 1, 516, 64, 64, [(13 * b) % 517 for b in range(40)], False),
+    (16, 64, 2, 1, 640, 128, 300, [40 * b for b in range(16)], True),   # as many rows as the join gives a warp each
+]
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "e4m3", "int8"])
+@pytest.mark.parametrize("B,Hq,Hkv,Nq,cap,D,Np,lens,causal", PREFIX_DIVIDED)
+def test_divided_caches_behind_a_prefix(fmt, B, Hq, Hkv, Nq, cap, D, Np, lens, causal):
+    dev = _gpu()
+    kc, vc, ks, vs = filled(B, Hkv, cap, D, fmt, lens, dev, seed=51)
+    q = rows(B, Hq, Nq, D, 52)
+    pk, pv = rows(1, Hkv, Np, D, 53)[0].contiguous(), rows(1, Hkv, Np, D, 54)[0].contiguous()
+    got = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs, pk, pv, causal=causal)
+    assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
+    check_decode(q, kc, vc, ks, vs, ints(*lens), got, causal, pk=pk, pv=pv)
