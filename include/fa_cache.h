@@ -9,8 +9,9 @@
  *   FA_CACHE_BF16  bf16 values
  *   FA_CACHE_E4M3  1-byte e4m3 codes (OCP FP8 E4M3) with one fp32 scale a row
  *   FA_CACHE_INT8  1-byte signed codes with one fp32 scale a row
- * k_scale, v_scale fp32 [B, Hkv, capacity] (NULL for bf16), >= 0 or NaN: a code
- * stands for code * scale.  The writer's rules, for a row with largest magnitude amax:
+ * k_scale, v_scale fp32 [B, Hkv, capacity] (NULL for bf16), from 0 to 2^126 or
+ * NaN: a code stands for code * scale.  The writer's rules, for a row with
+ * largest magnitude amax:
  *   e4m3  scale = 2^e with the smallest e >= -120 such that amax <= 448 * 2^e
  *         (dividing by it is exact, so a value is rounded once, to the nearest
  *         code, ties to even; a scale that is no power of two would gain no
@@ -51,14 +52,16 @@ typedef struct {
  * NULL: all N rows).  k, v: bf16 views [B,Hkv,N,D] (see fa_rows; v may have
  * other strides than k).  start, count: int32 [B] on the device.  Rows whose
  * slot is not in 0 .. capacity - 1 are dropped; slots that no row goes to are
- * left as they are.  Caches 16-byte aligned, scales 16-byte. */
+ * left as they are.  Caches 16-byte aligned, scales 16-byte.  k and v share no
+ * memory with the caches (rows are not moved within one). */
 FA_API fa_status fa_cache_write(const fa_cache_shape* shape, int N, const fa_rows* k, const fa_rows* v,
                                 const int* start, const int* count, void* k_cache, void* v_cache, float* k_scale,
                                 float* v_scale, void* stream);
 
 /* Reads slots 0 .. N - 1 of every sequence back: k_out, v_out bf16
  * [B,Hkv,N,D] contiguous, bf16(code * scale); rows at or behind lens[b]
- * (int32 [B] on the device; NULL: capacity) become 0.  1 <= N <= capacity. */
+ * (int32 [B] on the device; NULL: capacity) become 0.  1 <= N <= capacity.  The
+ * outputs share no memory with the cache. */
 FA_API fa_status fa_cache_read(const fa_cache_shape* shape, int N, const int* lens, const void* k_cache,
                                const void* v_cache, const float* k_scale, const float* v_scale, void* k_out,
                                void* v_out, void* stream);

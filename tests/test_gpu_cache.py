@@ -777,3 +777,16 @@ def test_divided_caches_behind_a_prefix(fmt, B, Hq, Hkv, Nq, cap, D, Np, lens, c
     got = cache.decode_cache(q, kc, vc, ints(*lens), ks, vs, pk, pv, causal=causal)
     assert A.device_status(dev) == A.FA_OK, f"sites {A.timeout_sites():#x}"
     check_decode(q, kc, vc, ks, vs, ints(*lens), got, causal, pk=pk, pv=pv)
+
+
+@pytest.mark.parametrize("fmt", ["bf16", "int8"])
+def test_reading_no_slots(fmt):
+    """The history of sequences that have none yet, as writing no rows."""
+    dev = _gpu()
+    kc, vc, ks, vs = filled(2, 3, 64, 64, fmt, [64, 5], dev)
+    k, v = cache.cache_read(kc, vc, 0, lens=ints(0, 0), k_scale=ks, v_scale=vs)
+    assert k.shape == v.shape == (2, 3, 0, 64) and k.dtype == torch.bfloat16 and k.is_cuda
+    with pytest.raises((TypeError, ValueError, RuntimeError)):
+        cache.cache_read(kc, vc, -1, k_scale=ks, v_scale=vs)
+    with pytest.raises((TypeError, ValueError)):
+        cache.cache_read(kc, vc, 0, lens=[0, 0], k_scale=ks, v_scale=vs)

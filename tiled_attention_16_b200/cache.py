@@ -156,6 +156,8 @@ def cache_read(k_cache: torch.Tensor, v_cache: torch.Tensor, n: int | None = Non
         out_v = torch.empty(shape, dtype=torch.bfloat16, device=k_cache.device)
     else:
         want(out_v, "out_v", shape, torch.bfloat16, k_cache)
+    if n == 0:
+        return out_k, out_v
     shp = FaCacheShape(B, Hkv, cap, D, fmt)
     st = _cache_lib().fa_cache_read(ctypes.byref(shp), n, None if lens is None else lens.data_ptr(),
                                     k_cache.data_ptr(), v_cache.data_ptr(), ks, vs, out_k.data_ptr(),
