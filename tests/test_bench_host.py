@@ -147,6 +147,13 @@ def test_committed_traffic_record_parses():
     assert len(entries) >= 6
 
 
+@pytest.mark.parametrize("kernel,workload", [("fa_fwd_kernel", "long"), ("fa_bwd_fused_kernel", "long"),
+                                             ("fa_fwd_fp8_kernel", "long"), ("fa_decode_split_kernel", "decode70b")])
+def test_committed_traffic_record_is_of_the_current_sources(kernel, workload):
+    # otherwise bench.py reports no traffic: capture it again (commands in profiles/dram_traffic_<workload>.md)
+    assert bench.recorded_traffic(kernel, workload) is not None
+
+
 @pytest.mark.parametrize("ws", [1, 2, 8])
 def test_job_throughput_counts_every_rank(ws):
     # flops of one step on each rank, over the slowest rank's time

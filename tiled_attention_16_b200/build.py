@@ -16,7 +16,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libfa_sm100.so")
 SOURCES = ["fa_api.cu", "fa_fwd.cu", "fa_fwd_pair.cu", "fa_fwd_fp8.cu", "fa_bwd.cu", "fa_bwd_split.cu", "fa_bwd_fused.cu", "fa_bwd_pair.cu", "fa_decode.cu", "fa_cp.cu", "fa_selftest.cu",
            "fa_rope.cu", "fa_cache.cu", "fa_cache_decode.cu", "fa_prefix.cu", "fa_cache_api.cu"]
-HEADERS = ["sm100.cuh", "fa_internal.h"]
+HEADERS = ["sm100.cuh", "fa_internal.h", "fa_serving.cuh"]
 PUBLIC = ["fa.h", "fa_rope.h", "fa_cache.h"]
 
 NVCC_FLAGS = [

@@ -6,8 +6,7 @@
 // 71 us, 5.8 TB/s; 3548 slots back: 103 us, 6.6).  D / 8 lanes hold a row, 8 values each (16-byte accesses on
 // the bf16 side, 8-byte on the codes); a thread takes kRows rows and issues
 // their loads together.  blockIdx.y is 0 for K and 1 for V.
-#include "fa_internal.h"
-#include "sm100.cuh"
+#include "fa_serving.cuh"
 
 #include <cuda_bf16.h>
 #include <cuda_fp8.h>

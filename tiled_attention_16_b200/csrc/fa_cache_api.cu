@@ -2,8 +2,8 @@
 // argument checks, plans, tensor maps and launches.  No device memory is
 // allocated here; every buffer belongs to the caller.
 #include "fa_cache.h"
-#include "fa_internal.h"
 #include "fa_rope.h"
+#include "fa_serving.cuh"
 
 #include <algorithm>
 #include <cmath>

@@ -41,8 +41,7 @@
 // of a key with one shared-memory load and uses them as its four k-steps; for
 // V, ldmatrix.trans moves pairs of codes and a byte permute makes the two
 // rows d, d + 1 of V^T from them.
-#include "fa_internal.h"
-#include "sm100.cuh"
+#include "fa_serving.cuh"
 
 #include <cfloat>
 

@@ -1,11 +1,9 @@
 // fa_internal.h — launch interface shared by the host API and the kernels.
 #pragma once
 
-#include <atomic>
 #include <cstddef>
 #include <cstdint>
 #include <cuda.h>
-#include <cuda_bf16.h>
 #include <cuda_runtime.h>
 
 namespace fa {
@@ -160,127 +158,5 @@ cudaError_t launch_bwd_dq_convert(const float* dq_acc, void* dq, size_t n_elems,
 cudaError_t launch_lse_merge(int D, long long rows, const void* o_part, const float* lse_part, float* o_acc,
                              float* lse_acc, void* o_out, int first, cudaStream_t stream);
 cudaError_t launch_accumulate(long long n, const void* src, float* acc, void* out, int first, cudaStream_t stream);
-
-// Raises a kernel's dynamic shared memory limit, once per device (the call
-// costs about as much as half a launch).
-struct SmemOptIn {
-    std::atomic<bool> done[64] = {};
-    cudaError_t set(const void* kernel, int bytes) {
-        int dev = 0;
-        cudaError_t e = cudaGetDevice(&dev);
-        if (e != cudaSuccess) return e;
-        const bool known = dev >= 0 && dev < 64;
-        if (known && done[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-        if (e == cudaSuccess && known) done[dev].store(true, std::memory_order_relaxed);
-        return e;
-    }
-};
-
-// Launch of a kernel that may start before the kernel ahead of it in the stream
-// has ended; it waits for it itself (grid_wait) where it needs its results, and
-// in any case before it ends.
-template <class... Params, class... Args>
-cudaError_t launch_dependent(void (*kernel)(Params...), unsigned grid, unsigned block, size_t smem, cudaStream_t stream,
-                             const Args&... args) {
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(block);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = stream;
-    cudaLaunchAttribute attr = {};
-    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr.val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = &attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
-// bf16 rows of D contiguous values, indexed [b, h, n] by strides in elements.
-struct RopeRows {
-    __nv_bfloat16* data;
-    long long stride_b, stride_h, stride_n;
-};
-
-// Per-head norm with rotation (fa_rope.cu); q_out / k_out are written by the
-// forward, the d* fields are the backward's.
-struct RopeParams {
-    RopeRows q, k, dq, dk;
-    __nv_bfloat16 *q_out, *k_out;
-    const __nv_bfloat16 *dq_out, *dk_out;
-    const void *q_weight, *k_weight;
-    const float* inv_freq;
-    const int* positions;
-    float* dw_part;    // [CTAs, 2, D]
-    int Hq, Hkv, N, rot, weight_bf16;
-    float eps;
-    long long tokens;  // B * N
-    int token_slots, parts_q, parts_k, items_q, n_items;   // filled by the launch
-};
-int rope_bwd_ctas(int sms);
-cudaError_t launch_qk_norm_rope(int D, int interleaved, RopeParams p, int sms, cudaStream_t stream);
-cudaError_t launch_qk_norm_rope_bwd(int D, int interleaved, RopeParams p, float* dqw, float* dkw, int sms,
-                                    cudaStream_t stream);
-
-// Cache writes and reads (fa_cache.cu).
-struct CacheWriteParams {
-    RopeRows k, v;
-    const int *start, *count;
-    void *k_cache, *v_cache;
-    float *k_scale, *v_scale;
-    int B, H, N, capacity;
-    int shift;               // log2 of a tile's heads; filled by the launch
-};
-struct CacheReadParams {
-    const void *k_cache, *v_cache;
-    const float *k_scale, *v_scale;
-    const int* lens;
-    void *k_out, *v_out;
-    int BH, H, N, capacity;
-};
-cudaError_t launch_cache_write(int D, int fmt, CacheWriteParams p, cudaStream_t stream);
-cudaError_t launch_cache_read(int D, int fmt, const CacheReadParams& p, cudaStream_t stream);
-
-// Decoding over a cache (fa_cache_decode.cu).
-struct CacheDecodeParams {
-    const void* q;           // bf16 [B,Hq,Nq,D]
-    void* o;                 // bf16 [B,Hq,Nq,D]
-    float* lse;              // fp32 [B,Hq,Nq]
-    const int* lens;
-    const float *k_scale, *v_scale;
-    const void* v_cache;     // read directly where a bf16 row holds an infinity or a NaN
-    float *o_part, *lse_part;  // parts of units shared by CTAs: slots 2 c, 2 c + 1 of rows_cta rows each
-    float *o_unit, *lse_unit;  // [B*Hq*Nq, D], [B*Hq*Nq]: undivided units' results for the merge with the
-                               // prefix (null without one: they go to o and lse)
-    int2* meta;              // [B * Hkv * RB]: a unit's first slot (-1: undivided) and parts, for each row block
-                             // (null: no join follows)
-    int B, Hkv, G, Nq, capacity, causal;
-    int rows_cta, RB;        // query rows a CTA holds (8, 16 or 32), row blocks of a K/V head
-    int n_cta;
-    int unit_cost;           // positions a unit counts besides its tiles
-    int undivided;           // every unit is a run
-    float scale_log2;
-};
-// CTAs of the cache part that fit on an SM at once (shared memory and registers).
-int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta);
-int cache_decode_unit_cost(int rows_cta);
-// after_prefix: the prefix kernel is the one ahead of it in the stream.
-cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,
-                                const CacheDecodeParams& p, bool after_prefix, cudaStream_t stream);
-
-// Shared prefix (fa_prefix.cu).  A unit is rows_unit (128 or 256) of the
-// B * G * Nq rows of a K/V head; the part of unit u that CTA c computes lies in
-// slot c + u of rows_unit rows.
-struct PrefixParams {
-    const void* q;
-    float *o_part, *lse_part;
-    int B, Hkv, G, Nq, Np;
-    int rows_unit, n_rowtiles, n_tiles;
-    int n_cta;               // 0: no prefix
-    float scale_log2;
-};
-cudaError_t launch_prefix(int D, const CUtensorMap& tk, const CUtensorMap& tv, const PrefixParams& p,
-                          cudaStream_t stream);
-cudaError_t launch_cache_combine(int D, const CacheDecodeParams& p, const PrefixParams& f, cudaStream_t stream);
 
 }  // namespace fa

@@ -27,8 +27,7 @@
 //   warps 0-3, 4-7  Q rows to shared memory, softmax, epilogue of block 0, 1
 //   warp  8         MMA issuer     warp 9  TMA producer of the K/V ring
 //   S0 | S1 | O0 | O1, 128 columns each; P over S as packed bf16
-#include "fa_internal.h"
-#include "sm100.cuh"
+#include "fa_serving.cuh"
 
 #include <cuda_bf16.h>
 

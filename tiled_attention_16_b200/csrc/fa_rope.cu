@@ -13,8 +13,7 @@
 // go through packed fp32 arithmetic, and the weights and the turn are one 2 x 2
 // matrix a pair.  8 x 2048 tokens of 64 heads of 128: forward 91 us (5.9 TB/s),
 // backward 144 us (5.6 TB/s).
-#include "fa_internal.h"
-#include "sm100.cuh"
+#include "fa_serving.cuh"
 
 #include <climits>
 
