@@ -1,10 +1,12 @@
 // fa_cache.cu — writing K/V rows into a cache at 16 or 8 bits, and reading
 // them back (include/fa_cache.h has the formats and the rounding rules).
 //
-// Bound by HBM: a write reads 2 bytes an element and writes 1 or 2, a read the
-// other way round (8 sequences of 2048 tokens, 32 heads of 128, e4m3: write
-// 71 us, 5.8 TB/s; 3548 slots back: 103 us, 6.6).  D / 8 lanes hold a row, 8 values each (16-byte accesses on
-// the bf16 side, 8-byte on the codes); a thread takes kRows rows and issues
+// A write reads 2 bytes an element and writes 1 or 2, a read the other way round.
+// 8 sequences of 2048 tokens, 32 heads of 128: bf16 write 82 us (6.6 TB/s), e4m3
+// 71 (5.8), both bound by HBM; int8 130 us for the bytes of e4m3, bound by the
+// instructions of its rounding (code_int8).  3548 slots back: e4m3 and int8 103 us
+// (6.6 TB/s), bf16 132.  D / 8 lanes hold a row, 8 values each (16-byte accesses
+// on the bf16 side, 8-byte on the codes); a thread takes kRows rows and issues
 // their loads together.  blockIdx.y is 0 for K and 1 for V.
 #include "fa_serving.cuh"
 

@@ -112,7 +112,8 @@ bool cache_pointers_ok(int format, const void* kc, const void* vc, const float* 
 
 // Query rows of a K/V head a CTA of the cache part holds, of R.
 // 8 sequences of 32K slots of 8 heads of 128, with 32 rows a CTA and with twice
-// 16: 24 int8 rows 142 and 170 us, 32 rows e4m3 153 and 150, bf16 168 and 188.
+// 16: 24 int8 rows 142 and 170 us, 32 rows e4m3 153 and 150, bf16 168 and 188 (171
+// now that V rows hidden from some queries are looked at).
 int rows_of_cta(long long R) { return R <= 8 ? 8 : R <= 16 ? 16 : 32; }
 // Rows of a unit of the prefix part, of head_rows: two row tiles share the key
 // tiles where there are two.
@@ -140,9 +141,12 @@ fa_status check_decode(const fa_cache_decode_shape* s) {
 
 // Capacity up to which a (sequence, K/V head) is one CTA's: no join is needed
 // then, which saves a launch.  Measured with 32 query over 8 K/V heads and 1, 8,
-// 64 sequences of e4m3 slots, device time undivided and divided: 256 slots 6.0,
-// 6.1, 13.9 us and 8.3, 9.1, 15.0; 512 slots 8.1, 8.2, 21.7 and 8.5, 10.0, 20.5;
-// 1024 slots 12.1, 12.2, 35.6 and 9.1, 10.7, 31.5.
+// 64 sequences, device time in us undivided and divided:
+//               256 slots                      512 slots                      1024 slots
+//   e4m3 128    5.6  5.8 14.0,  8.2 9.2 15.1   7.7 8.0 22.3,  8.4 10.0 20.6   11.5 11.9 35.2,  9.0 10.8 31.4
+//   e4m3  64    5.4  5.5  7.3,  7.7 8.5 12.9   7.0 7.2 10.8,  8.2  9.0 16.4   10.2 10.4 18.3,  8.5  9.8 21.7
+//   bf16 128    5.8  5.9 17.8,  7.9 9.0 19.3   7.7 8.0 28.5,  8.3 10.0 29.2   11.7 14.6 48.9,  8.9 12.1 48.4
+//   bf16  64    5.1  5.4  8.1,  7.6 8.2 13.6   6.6 6.8 15.3,  8.0  9.0 19.1    9.7  9.8 25.3,  8.3  9.6 29.8
 constexpr int kUndividedSlots = FA_CACHE_UNDIVIDED;
 
 // How a decode call is split.  The cache part runs on as many CTAs as fit on

@@ -1082,9 +1082,13 @@ int cache_decode_ctas_per_sm(int D, int fmt, int rows_cta) {
     return rows_cta == 32 || (D == 128 && fmt == 0) ? 2 : 3;
 }
 
-// Measured with 64 sequences of up to 1000 slots (8 rows, with the join): 32.4 us
-// at 0, 24.6 at 1, 22.1 at 2; with 48 of up to 8100 (12 rows): 51.4 at 1, 47.8
-// at 2, 46.6 at 3, 46.2 at 4.
+// Measured at a cost of 0, 1, 2, 3, 4 and 6 with 64 sequences of up to 1000 slots
+// (8 rows, with the join): e4m3 at D = 128 31.9, 24.6, 22.0, 22.0, 22.3, 22.7 us, at
+// 64 27.5, 21.2, 17.5, 17.2, 16.9, 17.1; bf16 at 128 36.0, 31.5, 31.5, 31.5, 32.0,
+// 32.5, at 64 27.6, 21.0, 20.1, 20.4, 20.5, 20.9.  With 48 of up to 8100 (12 rows):
+// e4m3 at 128 52.7, 49.2, 46.2, 45.4, 45.6, 45.9, at 64 42.6, 39.9, 37.5, 34.9,
+// 33.8, 33.6; bf16 at 128 77.8, 73.8, 71.8, 71.7, 71.8, 72.6, at 64 50.4, 46.5,
+// 44.1, 43.2, 43.2, 43.1.
 int cache_decode_unit_cost(int rows_cta) { return rows_cta == 8 ? 2 : 4; }
 
 cudaError_t launch_cache_decode(int D, int fmt, const CUtensorMap& tk, const CUtensorMap& tv,

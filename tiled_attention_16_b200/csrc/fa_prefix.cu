@@ -18,10 +18,10 @@
 //             two accumulators are joined as they leave tensor memory
 // Up to 128 rows the work is bound by HBM whichever rows are real: a 64 KB
 // key tile costs about 1000 tensor cycles and, at the copy rate, 2800 cycles
-// (8 K/V heads of 32768 keys, 128 rows: 29 us, 4.6 TB/s with its start and
-// results).  512 rows of the same take 67 us: 2.15 us a key tile in the main
-// loop, 70% of the burst rate of a library product, with the SM clock at 1.6 to
-// 1.75 GHz under it.
+// (8 K/V heads, 128 rows: 32768 keys more take 19.4 us, 6.9 TB/s; the first 32768
+// 29 us, 4.6 TB/s with the start and the results).  512 rows of the same take
+// 67 us: 2.15 us a key tile in the main loop, 70% of the burst rate of a library
+// product, with the SM clock at 1.6 to 1.75 GHz under it.
 //
 // Warp roles (320 threads) and tensor memory as in fa_fwd.cu:
 //   warps 0-3, 4-7  Q rows to shared memory, softmax, epilogue of block 0, 1
