@@ -99,8 +99,9 @@ FA_API size_t fa_decode_cache_workspace_bytes(const fa_cache_decode_shape* shape
  * it as one matrix.  The 8-bit formats multiply in fp16 on the codes (exact
  * there), q scaled by a power of two for each row; scales enter in fp32.  P
  * times the V scales is rounded to fp16 (2^-11 of each weight, and for weights
- * far below the largest up to 2^-30 of the sequence's largest V value); with
- * bf16 caches and prefixes P is rounded to bf16 (2^-8).
+ * far below the largest up to 2^-30 of the largest V value below the sequence's
+ * length, seen by the query or not); with bf16 caches and prefixes P is rounded
+ * to bf16 (2^-8).
  * workspace: 256-byte aligned (NULL allowed where 0 bytes are needed), contents
  * on entry do not matter; calls that may overlap need workspaces of their own.
  * o, lse and the workspace share no memory with the inputs.  8-bit codes below a

@@ -150,7 +150,7 @@ def test_committed_traffic_record_parses():
 @pytest.mark.parametrize("kernel,workload", [("fa_fwd_kernel", "long"), ("fa_bwd_fused_kernel", "long"),
                                              ("fa_fwd_fp8_kernel", "long"), ("fa_decode_split_kernel", "decode70b")])
 def test_committed_traffic_record_is_of_the_current_sources(kernel, workload):
-    # otherwise bench.py reports no traffic: capture it again (commands in profiles/dram_traffic_<workload>.md)
+    # otherwise bench.py reports no traffic: a changed source asks for another capture
     assert bench.recorded_traffic(kernel, workload) is not None
 
 

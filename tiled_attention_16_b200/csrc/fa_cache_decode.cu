@@ -31,7 +31,8 @@
 // scales seen so far, is rounded to fp16 with its row maximum between 2^6 and
 // 2^14 (a value of 2^-20 of the maximum is still a normal number: relative
 // error 2^-11; below, the absolute one is 2^-31 of it); the row sum l is taken
-// before that.  With bf16 caches P is rounded to bf16 (2^-8).  The maximum in
+// before that.  With bf16 caches P is rounded to bf16 (2^-8): a product has one
+// operand type, and V's range does not fit fp16.  The maximum in
 // use is replaced only when a score exceeds it by more than 8 (log2 units), and
 // the bound on the V scales when one exceeds it, so most tiles need one vote
 // (which is the barrier) and no shuffles or rescaling.  All four warps use the

@@ -26,7 +26,9 @@
 // Warp roles (320 threads) and tensor memory as in fa_fwd.cu:
 //   warps 0-3, 4-7  Q rows to shared memory, softmax, epilogue of block 0, 1
 //   warp  8         MMA issuer     warp 9  TMA producer of the K/V ring
-//   S0 | S1 | O0 | O1, 128 columns each; P over S as packed bf16
+//   S0 | S1 | O0 | O1, 128 columns each; P over S as packed bf16 (2^-8 of each
+//   weight, as in the forward: V is bf16, and P in two bf16 parts would be half
+//   as many products again)
 #include "fa_serving.cuh"
 
 #include <cuda_bf16.h>
